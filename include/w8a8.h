@@ -56,6 +56,8 @@ typedef int32_t w8a8_status;
 #define W8A8_ERR_NOT_IMPLEMENTED 8
 #define W8A8_ERR_WORKSPACE 9          /* workspace missing or smaller than the query says */
 #define W8A8_ERR_NO_DEVICE 10         /* no usable sm_100 device is current */
+#define W8A8_ERR_BAD_PAGE 11          /* a page table entry outside the cache (device status) */
+#define W8A8_ERR_BAD_SEQUENCE 12      /* sequence offsets or lengths outside the call's limits (device status) */
 
 typedef int32_t w8a8_dtype;
 #define W8A8_BF16 0
@@ -409,6 +411,179 @@ w8a8_status int8_mixed_decomp_gemm_tc(const int8_t *Xq, const float *S_x, const 
 /* Bytes of device workspace int8_mixed_decomp_gemm_tc needs: (M + N) rows of
  * cap rounded up to a multiple of 64 bf16 values (0 for a bad shape). */
 size_t int8_mixed_decomp_gemm_tc_workspace_size(int64_t M, int64_t N, int32_t cap);
+
+/* --------------------------------------------------------------------------
+ * INT8 paged KV cache: append, read back, attention.
+ *
+ * Source: PDMIX glossary §3 (KVCache Quant, the companion of PDMIX) and PDMIX
+ * configuration guide (the W8A8C8 combination). The pages name the 8-bit
+ * cache and fix no scheme. w8a8_quant_per_tensor keeps a whole cache tensor
+ * under one static scale; the cache here is symmetric absmax int8 (the
+ * LLM.int8() summary's §一.1 equation) with one scale for each page of tokens
+ * and head, so that a page is written without calibration and an outlier
+ * token costs precision in its own page only.
+ *
+ * A cache holds `num_pages` pages of `page_size` tokens for each of
+ * `kv_heads` heads; k and v alike:
+ *   codes  int8 [num_pages, kv_heads, page_size, head_dim] dense, 16-byte aligned
+ *   scale  fp32 [num_pages, kv_heads]; value = scale * (float) code
+ * page_size is 16, 32, 64 or 128; head_dim is 64, 96 or 128.
+ *
+ * A batch of sequences: sequence b's token at position p lies at slot
+ * p % page_size of page page_table[b][p / page_size]. Its new tokens are rows
+ * seq_start[b] .. seq_start[b + 1] - 1 of the packed inputs of a call and are
+ * the LAST of its kv_len[b] tokens: row seq_start[b] + i has position
+ * kv_len[b] - (seq_start[b + 1] - seq_start[b]) + i. A row whose position is
+ * negative is padding (a captured decode step whose slot is empty has kv_len
+ * 0): it is not stored and sees no key. Rows at and past seq_start[batch]
+ * belong to no sequence; outputs keep what they held there.
+ *
+ * The lengths and the page table are read on the device, so one captured
+ * graph serves growing sequences. What the host cannot check is checked
+ * there: a sequence whose seq_start descends or passes the call's row count,
+ * that has more than max_q_len new tokens, or whose kv_len is negative or
+ * past max_kv_len is skipped (its outputs keep what they held) and sets
+ * W8A8_ERR_BAD_SEQUENCE in the device status word; a page table entry outside
+ * [0, num_pages) that is needed sets W8A8_ERR_BAD_PAGE, is not dereferenced,
+ * and its tokens are neither stored nor seen (read back as 0). Entries past
+ * a sequence's last page are not read.
+ *
+ * Several sequences may share pages that a call only reads. A page that
+ * w8a8_kv_append writes must belong to one sequence.
+ *
+ * All kernels use programmatic dependent launch; they touch the caller's
+ * memory only after the previous kernel on the stream has completed.
+ */
+typedef struct w8a8_kv_cache {
+  int8_t *k_codes, *v_codes; /* device int8 [num_pages, kv_heads, page_size, head_dim] */
+  float *k_scale, *v_scale;  /* device fp32 [num_pages, kv_heads] */
+  int64_t num_pages;
+  int32_t kv_heads, page_size, head_dim;
+} w8a8_kv_cache;
+
+typedef struct w8a8_kv_batch {
+  const int32_t *page_table; /* device int32 [batch, max_pages], row stride page_table_ld elements */
+  int64_t page_table_ld;
+  const int32_t *seq_start;  /* device int32 [batch + 1] */
+  const int32_t *kv_len;     /* device int32 [batch]: tokens of each sequence, the new ones included */
+  int32_t batch, max_pages;
+  int32_t max_q_len;         /* no sequence has more new tokens (host bound, chooses the kernel) */
+  int32_t max_kv_len;        /* no kv_len is larger; at most max_pages * page_size */
+} w8a8_kv_batch;
+
+/*
+ * Append the new tokens' keys and values, with the position rotation applied
+ * on the way; optionally rotate their queries too. For token row t at
+ * position p >= 0 (fp32, each operation rounded to nearest even):
+ *   rotation of x (keys and queries; values are not rotated), for
+ *   i < rot_dim / 2 with the pair (a, b) = (x[i], x[i + rot_dim / 2]), or
+ *   (x[2 i], x[2 i + 1]) when interleaved != 0:
+ *     a' = a cos[p][i] - b sin[p][i],  b' = b cos[p][i] + a sin[p][i]
+ *   (two products rounded, then their sum); other elements are unchanged.
+ *   q_out[t] = the rotated q[t] rounded to bf16 (all zeros for p < 0).
+ * For each page and head that receives tokens, with amax the largest
+ * magnitude among the new values in it:
+ *   S = max(S_old, amax / 127), S_old = 0 when the page's first slot is new
+ *   r = 1 / S (S = r = 0 when S == 0 or 1 / S overflows fp32)
+ *   new codes  = clamp(rne(x * r), -127, 127)
+ *   old codes of the page, when S > S_old: clamp(rne(code * (S_old / S)), -127, 127)
+ * so a page's scale only grows while it fills, and codes already in it are
+ * re-rounded when it does (each growth adds at most half a step of the new
+ * scale). Slots past the new tokens are not touched. Finite inputs are
+ * assumed, as everywhere in this library.
+ *   k, v    device bf16 [tokens, kv_heads, head_dim]; strides in elements
+ *           between tokens and between heads (multiples of 8, the heads of a
+ *           token may lie anywhere in a fused projection's row)
+ *   cos, sin  device fp32 [rope_len, rot_dim / 2] dense, 16-byte aligned;
+ *           both NULL: nothing is rotated. A sequence with kv_len > rope_len
+ *           is skipped (W8A8_ERR_BAD_SEQUENCE).
+ *   rot_dim a multiple of 16, 16 .. head_dim
+ *   q       device bf16 [tokens, q_heads, head_dim] with its strides, or NULL
+ *   q_out   device bf16 [tokens, q_heads, head_dim] dense, 16-byte aligned;
+ *           may be q itself when q is dense
+ * Nothing is written for tokens == 0. max_kv_len bounds kv_len as above.
+ */
+w8a8_status w8a8_kv_append(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch, int64_t tokens, const void *k,
+                           int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                           int64_t v_head_stride, const float *cos, const float *sin, int64_t rope_len,
+                           int32_t rot_dim, int32_t interleaved, const void *q, int64_t q_token_stride,
+                           int64_t q_head_stride, int32_t q_heads, void *q_out, void *stream);
+
+/*
+ * Read tokens back, the paged counterpart of w8a8_dequant_per_tensor: row
+ * row_start[b] + i of k_out and v_out is the token of sequence b at position
+ * first_pos[b] + i, scale * (float) code (one fp32 product), rounded to bf16
+ * or stored as fp32.
+ *   page_table  device int32 [batch, max_pages], row stride page_table_ld
+ *   first_pos   device int32 [batch];  row_start device int32 [batch + 1]
+ *   k_out, v_out  device [rows, kv_heads, head_dim] dense, 16-byte aligned;
+ *               one of them may be NULL. Rows at and past row_start[batch]
+ *               keep what they held.
+ * A sequence whose row_start descends or passes `rows`, or whose positions
+ * are not all in [0, max_pages * page_size), is skipped
+ * (W8A8_ERR_BAD_SEQUENCE).
+ */
+w8a8_status w8a8_kv_gather(const w8a8_kv_cache *cache, const int32_t *page_table, int64_t page_table_ld, int32_t batch,
+                           int32_t max_pages, const int32_t *first_pos, const int32_t *row_start, int64_t rows,
+                           void *k_out, void *v_out, w8a8_dtype out_dtype, void *stream);
+
+/* What a score is before the softmax, and which keys a query sees. */
+typedef struct w8a8_kv_scores {
+  float scale;               /* multiplies q . k; finite */
+  float softcap;             /* > 0: scores become softcap * tanh(score / softcap); 0: none */
+  const float *slopes;       /* device fp32 [q_heads] or NULL: adds -slopes[h] * (distance of query and key) */
+  int32_t window;            /* > 0: only keys less than `window` positions before the query; 0: no limit */
+  const int32_t *prefix_len; /* device int32 [batch] or NULL: keys at positions below it are seen by every query */
+} w8a8_kv_scores;
+
+/*
+ * Attention of the new tokens over the cache (into which they have been
+ * appended). For row t at position p of sequence b and head h, with kv head
+ * h / (q_heads / kv_heads), over the keys j < kv_len[b] with
+ * (j <= p and (window == 0 or p - j < window)) or j < prefix_len[b]:
+ *   s_j = cap(scale * (q . k_j)) - slopes[h] * (p - j)
+ *   out[t, h] = sum_j softmax(s)_j v_j       (0 for a padding row, p < 0)
+ * k_j and v_j are the values the codes stand for; scores, the running maximum
+ * and sum and the accumulation are fp32. Rounding: the codes enter the tensor
+ * cores exactly (an int8 code is exact in bf16) and the page's scales are
+ * applied in fp32. The weights times v's scale are rounded to bf16 for the
+ * second product: as a high and a low part where max_q_len * (q_heads /
+ * kv_heads) <= 32 (relative error 2^-16), and once beyond (2^-8 each, the
+ * error of a sum of n such terms growing like sqrt(n) against n).
+ *   q      device bf16 [tokens, q_heads, head_dim], strides in elements
+ *          (multiples of 8)
+ *   out    device bf16 [tokens, q_heads, head_dim] dense, 16-byte aligned
+ *   workspace  device, >= w8a8_kv_attention_workspace_size(...) bytes,
+ *          16-byte aligned; no initial contents needed, and calls that may
+ *          overlap on the GPU must not share it
+ * q_heads is a multiple of kv_heads, at most 128 times it. The result does
+ * not depend on what else runs on the device: partial results are joined in
+ * a fixed order.
+ */
+w8a8_status w8a8_kv_attention(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch, int64_t tokens, const void *q,
+                              int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads,
+                              const w8a8_kv_scores *scores, void *out, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * w8a8_kv_attention whose result is handed to the output projection already
+ * quantized with that linear's static parameters:
+ *   codes_out[t, h, d] = clamp(rne(float(bf16(out[t, h, d])) * r_out) + Z_out, -128, 127)
+ * identical to w8a8_kv_attention followed by w8a8_quant_per_tensor(out,
+ * r_out, Z_out) on its rows.
+ * Source: PDMIX glossary §2.3 eq. Q_decode, as for w8a8_linear_static_requant.
+ *   r_out, Z_out  device scalars of the next linear (w8a8_calibrate_static)
+ *   codes_out     device int8 [tokens, q_heads, head_dim] dense, 16-byte aligned
+ */
+w8a8_status w8a8_kv_attention_requant(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch, int64_t tokens,
+                                      const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads,
+                                      const w8a8_kv_scores *scores, const float *r_out, const int32_t *Z_out,
+                                      int8_t *codes_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace the two attention calls need on the current
+ * device (0 for arguments they refuse, and where they need none). */
+size_t w8a8_kv_attention_workspace_size(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch, int64_t tokens,
+                                        int32_t q_heads);
 
 /*
  * Device status word. Kernels record device-side failures (a bounded wait

@@ -142,6 +142,8 @@ const char *w8a8_status_string(w8a8_status s) {
     case W8A8_ERR_NOT_IMPLEMENTED: return "W8A8_ERR_NOT_IMPLEMENTED";
     case W8A8_ERR_WORKSPACE: return "W8A8_ERR_WORKSPACE";
     case W8A8_ERR_NO_DEVICE: return "W8A8_ERR_NO_DEVICE";
+    case W8A8_ERR_BAD_PAGE: return "W8A8_ERR_BAD_PAGE";
+    case W8A8_ERR_BAD_SEQUENCE: return "W8A8_ERR_BAD_SEQUENCE";
     default: return "W8A8_ERR_UNKNOWN";
   }
 }

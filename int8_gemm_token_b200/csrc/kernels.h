@@ -125,6 +125,67 @@ cudaError_t launch_outlier_split(const uint16_t *X, int64_t M, int64_t K, int64_
                                  int num_sms, int32_t *status, cudaStream_t s);
 size_t outlier_workspace_bytes(int64_t K);
 
+// ---------------------------------------------------------------- INT8 paged KV cache
+// Device view of a cache (w8a8_kv_cache) and of a batch (w8a8_kv_batch).
+struct KvCache {
+  int8_t *k = nullptr, *v = nullptr;  // [pages, heads, page, d]
+  float *ks = nullptr, *vs = nullptr;  // [pages, heads]
+  int64_t pages = 0;
+  int32_t heads = 0, page = 0, page_shift = 0, d = 0;
+};
+struct KvSeqs {
+  const int32_t *table = nullptr;
+  int64_t table_ld = 0;
+  const int32_t *seq_start = nullptr, *kv_len = nullptr;
+  int32_t batch = 0, max_pages = 0, max_q = 0, max_kv = 0;
+  int64_t tokens = 0;  // packed rows of the call
+};
+// A packed bf16 input [tokens, heads, d] with its strides in elements.
+struct KvRows {
+  const uint16_t *p = nullptr;
+  int64_t token_stride = 0, head_stride = 0;
+};
+struct KvAppendArgs {
+  KvCache c;
+  KvSeqs s;
+  KvRows k, v, q;
+  const float *cos = nullptr, *sin = nullptr;
+  int32_t rot = 0, interleaved = 0, q_heads = 0;
+  int32_t len_limit = 0;  // largest kv_len accepted
+  uint16_t *q_out = nullptr;
+  int32_t *status = nullptr;
+};
+cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
+
+struct KvGatherArgs {
+  KvCache c;
+  const int32_t *table = nullptr;
+  int64_t table_ld = 0;
+  int32_t batch = 0, max_pages = 0;
+  const int32_t *first_pos = nullptr, *row_start = nullptr;
+  int64_t rows = 0;
+  void *k_out = nullptr, *v_out = nullptr;
+  int32_t *status = nullptr;
+};
+cudaError_t launch_kv_gather(const KvGatherArgs &a, bool bf16_out, int num_sms, cudaStream_t s);
+
+struct KvAttnArgs {
+  KvCache c;
+  KvSeqs s;
+  KvRows q;
+  int32_t q_heads = 0, group = 0;  // group = q_heads / kv heads
+  float scale = 1.0f, softcap = 0.0f;
+  const float *slopes = nullptr;
+  int32_t window = 0;
+  const int32_t *prefix = nullptr;
+  void *out = nullptr;              // bf16, or int8 codes when r_out != nullptr
+  const float *r_out = nullptr;
+  const int32_t *z_out = nullptr;
+  int32_t *status = nullptr;
+};
+size_t kv_decode_workspace_bytes(const KvAttnArgs &a, int num_sms);
+cudaError_t launch_kv_decode(const KvAttnArgs &a, void *workspace, int num_sms, cudaStream_t s);
+
 // Per-device set-up of the C ABI (done once per device): SM count and the
 // device address of the device status word.
 w8a8_status current_device_info(int *sm_count, int32_t **status_word);

@@ -1,0 +1,384 @@
+// kv_cache.cu -- writing and reading the INT8 paged KV cache.
+//
+// What it computes (include/w8a8.h, w8a8_kv_append and w8a8_kv_gather): the
+// position rotation of new keys and queries, the symmetric absmax int8
+// quantization of new keys and values with one scale for each page and head
+// (LLM.int8() summary §一.1), and value = scale * code back.
+//
+// How (sm_100a): both are HBM streams with a data-dependent address, so the
+// work is cut where the addresses are: a UNIT is one page of one head of k or
+// of v, held by one group of threads that reads its new tokens once into
+// registers (rotated there), reduces their absmax, settles the page's scale
+// and writes the codes. Nothing is read twice and no atomic is needed: a page
+// and head belong to one group.
+//   Few new tokens a sequence (at most kFewTokens: decode steps): the group
+//   is one warp per (sequence, head, k or v), which walks the one or two
+//   pages its tokens touch.
+//   Many: the group is a block of 256 threads per page. Packed rows are cut
+//   into pages of their sequences by a search over
+//   f(b) = seq_start[b] / page + 2 b, which leaves each sequence room for
+//   the pages its tokens can touch (at most q / page + 2).
+// Within a group, D / 16 neighbouring threads hold one token: each takes the
+// two 8-element chunks of which one holds the first and one the second
+// elements of its pairs (or both whole pairs when interleaved), so a rotation
+// needs no exchange.
+#include "kv_common.cuh"
+
+namespace w8a8 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kFewTokens = 8;
+
+// 8 bf16 from global memory as fp32.
+__device__ __forceinline__ void load8(const uint16_t *p, float *x) {
+  const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(w[i]);
+    x[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+__device__ __forceinline__ void load8f(const float *p, float *x) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// The two 8-element chunks of unit u (of D / 16): pairs lie across them
+// (halves of the rotated part) or inside them (interleaved, and the part that
+// is not rotated).
+__device__ __forceinline__ void unit_chunks(int u, int rot, bool interleaved, int &c0, int &c1) {
+  const int nr = rot >> 4;  // units of the rotated part
+  if (!interleaved && u < nr) {
+    c0 = u;
+    c1 = u + nr;
+  } else {
+    c0 = 2 * u;
+    c1 = c0 + 1;
+  }
+}
+
+// Rotates the 16 values of unit u (x[0..7] of chunk c0, x[8..15] of c1) with
+// the 8 angles of the unit; products and sums rounded one by one.
+__device__ __forceinline__ void rotate16(float (&x)[16], const float (&c)[8], const float (&s)[8], bool interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = x[2 * i], b = x[2 * i + 1];
+      x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
+      x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = x[i], b = x[8 + i];
+      x[i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
+      x[8 + i] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+    }
+  }
+}
+
+__device__ __forceinline__ uint2 codes8(const float *x, float r) {
+  return make_uint2(low_bytes4(quant_sym(x[0], r), quant_sym(x[1], r), quant_sym(x[2], r), quant_sym(x[3], r)),
+                    low_bytes4(quant_sym(x[4], r), quant_sym(x[5], r), quant_sym(x[6], r), quant_sym(x[7], r)));
+}
+
+// Codes of a page re-rounded for its larger scale: clamp(rne(code * ratio), -127, 127).
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+  return low_bytes4(
+      quant_sym(static_cast<float>(sext_byte<0>(w)), ratio), quant_sym(static_cast<float>(sext_byte<1>(w)), ratio),
+      quant_sym(static_cast<float>(sext_byte<2>(w)), ratio), quant_sym(static_cast<float>(sext_byte<3>(w)), ratio));
+}
+
+// One unit: tokens [lo, hi) (positions) of sequence `seq`, all in page index
+// `pi`, head h of k (which == 0) or v. G threads (a warp or the block) of
+// which this is thread `tid`; PASSES * (G / U) covers the tokens of a page.
+template <int D, int G, int PASSES>
+__device__ __forceinline__ void append_unit(const KvAppendArgs &a, const KvSeq &seq, const int32_t *table_row, int pi,
+                                            int lo, int hi, int h, int which, int tid, float *s_red) {
+  constexpr int U = D / 16, TP = G / U;  // threads of a token, tokens of a pass
+  const int32_t page = load_page(table_row, pi, a.c.pages, a.status);
+  if (page < 0) return;  // uniform over the group: every thread read the same entry
+  const KvRows &src = which ? a.v : a.k;
+  int8_t *codes = (which ? a.c.v : a.c.k) + ((static_cast<int64_t>(page) * a.c.heads + h) << a.c.page_shift) * D;
+  float *scale = (which ? a.c.vs : a.c.ks) + static_cast<int64_t>(page) * a.c.heads + h;
+  const int old = lo & (a.c.page - 1);  // tokens that lie in the page already
+  const float s_old = old > 0 ? *scale : 0.0f;
+  const int u = tid % U, tok = tid / U;
+  const bool turn = a.cos != nullptr && which == 0;
+  const bool il = a.interleaved != 0;
+  const int rot = turn ? a.rot : 0;
+  int c0, c1;
+  unit_chunks(u, rot, il, c0, c1);
+  float x[PASSES][16];
+  float amax = 0.0f;
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int pos = lo + p * TP + tok;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[p][i] = 0.0f;
+    if (tok < TP && pos < hi) {
+      const uint16_t *row = src.p + (seq.row0 + pos - seq.pos0()) * src.token_stride + h * src.head_stride;
+      load8(row + 8 * c0, x[p]);
+      load8(row + 8 * c1, x[p] + 8);
+      if (16 * u < rot) {
+        float cs[8], sn[8];
+        const int64_t at = static_cast<int64_t>(pos) * (a.rot >> 1) + 8 * u;
+        load8f(a.cos + at, cs);
+        load8f(a.sin + at, sn);
+        rotate16(x[p], cs, sn, il);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[p][i]));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  if constexpr (G > 32) {
+    if ((tid & 31) == 0) s_red[tid >> 5] = amax;
+    __syncthreads();  // also: every thread has read the old scale
+#pragma unroll
+    for (int w = 0; w < G / 32; ++w) amax = fmaxf(amax, s_red[w]);
+  } else {
+    __syncwarp();
+  }
+  float S = fmaxf(s_old, __fdiv_rn(amax, 127.0f));
+  float r = S > 0.0f ? __fdiv_rn(1.0f, S) : 0.0f;
+  if (isinf(r)) S = r = 0.0f;
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int pos = lo + p * TP + tok;
+    if (tok < TP && pos < hi) {
+      int8_t *row = codes + (pos & (a.c.page - 1)) * D;
+      *reinterpret_cast<uint2 *>(row + 8 * c0) = codes8(x[p], r);
+      *reinterpret_cast<uint2 *>(row + 8 * c1) = codes8(x[p] + 8, r);
+    }
+  }
+  if (old > 0 && S != s_old) {
+    const float ratio = S > 0.0f ? __fdiv_rn(s_old, S) : 0.0f;
+    for (int i = tid; i < old * U; i += G) {
+      uint4 *w = reinterpret_cast<uint4 *>(codes) + i;
+      const uint4 v = *w;
+      *w = make_uint4(rescale4(v.x, ratio), rescale4(v.y, ratio), rescale4(v.z, ratio), rescale4(v.w, ratio));
+    }
+  }
+  if (tid == 0 && (old == 0 || S != s_old)) *scale = S;
+}
+
+// Rotation of one query row (all heads) by one warp; t a packed row.
+template <int D>
+__device__ __forceinline__ void rotate_query_row(const KvAppendArgs &a, int64_t t) {
+  constexpr int U = D / 16, HP = 32 / U;  // lanes of a head, heads of a pass
+  const int lane = threadIdx.x & 31;
+  const int32_t *next = a.s.seq_start + 1;
+  const int32_t b = warp_count_le([&](int32_t i) { return static_cast<int64_t>(__ldg(next + i)); }, a.s.batch, t);
+  if (b >= a.s.batch) return;  // behind the last sequence
+  const KvSeq seq = load_seq(a.s, b, a.len_limit, a.status);
+  const int64_t i = t - seq.row0;
+  if (i < 0 || i >= seq.q) return;
+  const int64_t pos = seq.pos0() + i;
+  const int u = lane % U, hl = lane / U;
+  const bool il = a.interleaved != 0;
+  int c0, c1;
+  unit_chunks(u, a.rot, il, c0, c1);
+  const bool turn = a.cos != nullptr && 16 * u < a.rot && pos >= 0;
+  float cs[8], sn[8];
+  if (turn) {
+    const int64_t at = pos * (a.rot >> 1) + 8 * u;
+    load8f(a.cos + at, cs);
+    load8f(a.sin + at, sn);
+  }
+  if (hl >= HP) return;
+  for (int h = hl; h < a.q_heads; h += HP) {
+    const uint16_t *row = a.q.p + t * a.q.token_stride + h * a.q.head_stride;
+    uint16_t *out = a.q_out + (t * a.q_heads + h) * D;
+    float x[16];
+    if (pos >= 0) {
+      load8(row + 8 * c0, x);
+      load8(row + 8 * c1, x + 8);
+      if (turn) rotate16(x, cs, sn, il);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = 0.0f;
+    }
+    *reinterpret_cast<uint4 *>(out + 8 * c0) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                          pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    *reinterpret_cast<uint4 *>(out + 8 * c1) = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]),
+                                                          pack_bf16x2(x[12], x[13]), pack_bf16x2(x[14], x[15]));
+  }
+}
+
+// Few new tokens a sequence: warps [0, batch * heads * 2) one (sequence,
+// head, k or v) each, the following warps one query row each.
+template <int D>
+__global__ void __launch_bounds__(kThreads) append_few_kernel(const __grid_constant__ KvAppendArgs a) {
+  pdl_launch_dependents();
+  pdl_wait_prerequisite();
+  const int lane = threadIdx.x & 31;
+  int64_t w = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
+  const int64_t units = static_cast<int64_t>(a.s.batch) * a.c.heads * 2;
+  if (w >= units) {
+    w -= units;
+    if (a.q_out && w < a.s.tokens) rotate_query_row<D>(a, w);
+    return;
+  }
+  const int which = static_cast<int>(w & 1);
+  w >>= 1;
+  const int h = static_cast<int>(w % a.c.heads), b = static_cast<int>(w / a.c.heads);
+  const KvSeq seq = load_seq(a.s, b, a.len_limit, a.status);
+  if (seq.q == 0) return;
+  const int32_t *row = a.s.table + b * a.s.table_ld;
+  constexpr int TP = 32 / (D / 16), PASSES = (kFewTokens + TP - 1) / TP;
+  for (int lo = max(seq.pos0(), 0); lo < seq.n;) {
+    const int pi = lo >> a.c.page_shift;
+    const int hi = min(seq.n, (pi + 1) << a.c.page_shift);
+    append_unit<D, 32, PASSES>(a, seq, row, pi, lo, hi, h, which, lane, nullptr);
+    lo = hi;
+  }
+}
+
+// Many new tokens: blocks [0, tiles * heads * 2) one page of one head of k or
+// v each (blocks whose page does not exist leave), the following blocks 8
+// query rows each.
+template <int D>
+__global__ void __launch_bounds__(kThreads) append_pages_kernel(const __grid_constant__ KvAppendArgs a, int64_t tiles) {
+  __shared__ float s_red[kThreads / 32];
+  pdl_launch_dependents();
+  pdl_wait_prerequisite();
+  const int64_t units = tiles * a.c.heads * 2;
+  if (blockIdx.x >= units) {
+    const int64_t t = (blockIdx.x - units) * (kThreads / 32) + (threadIdx.x >> 5);
+    if (t < a.s.tokens) rotate_query_row<D>(a, t);
+    return;
+  }
+  const int64_t per = a.c.heads * 2;
+  const int64_t tile = blockIdx.x / per;
+  const int which = static_cast<int>(blockIdx.x & 1), h = static_cast<int>((blockIdx.x % per) >> 1);
+  const int shift = a.c.page_shift;
+  const auto f = [&](int32_t i) { return static_cast<int64_t>(__ldg(a.s.seq_start + i) >> shift) + 2 * int64_t(i); };
+  const int32_t b = warp_count_le(f, a.s.batch, tile) - 1;
+  if (b < 0) return;
+  const KvSeq seq = load_seq(a.s, b, a.len_limit, a.status);
+  if (seq.q == 0) return;
+  const int start = max(seq.pos0(), 0);
+  const int64_t pi = (start >> shift) + (tile - f(b));
+  if (start >= seq.n || pi > ((seq.n - 1) >> shift)) return;
+  const int lo = max(start, static_cast<int>(pi) << shift);
+  const int hi = min(seq.n, static_cast<int>((pi + 1) << shift));
+  constexpr int TP = kThreads / (D / 16), PASSES = (128 + TP - 1) / TP;
+  append_unit<D, kThreads, PASSES>(a, seq, a.s.table + b * a.s.table_ld, static_cast<int>(pi), lo, hi, h, which,
+                                   threadIdx.x, s_red);
+}
+
+cudaLaunchConfig_t pdl_config(int64_t blocks, cudaStream_t s, cudaLaunchAttribute *attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <int D>
+cudaError_t launch_append_t(const KvAppendArgs &a, cudaStream_t s) {
+  cudaLaunchAttribute attr;
+  if (a.s.max_q <= kFewTokens) {
+    const int64_t warps = static_cast<int64_t>(a.s.batch) * a.c.heads * 2 + (a.q_out ? a.s.tokens : 0);
+    const cudaLaunchConfig_t cfg = pdl_config((warps + kThreads / 32 - 1) / (kThreads / 32), s, &attr);
+    return cudaLaunchKernelEx(&cfg, append_few_kernel<D>, a);
+  }
+  const int64_t tiles = (a.s.tokens >> a.c.page_shift) + 2 * static_cast<int64_t>(a.s.batch);
+  const int64_t blocks = tiles * a.c.heads * 2 + (a.q_out ? (a.s.tokens + kThreads / 32 - 1) / (kThreads / 32) : 0);
+  const cudaLaunchConfig_t cfg = pdl_config(blocks, s, &attr);
+  return cudaLaunchKernelEx(&cfg, append_pages_kernel<D>, a, tiles);
+}
+
+// ------------------------------------------------------------------ gather
+// One warp per kGatherRows consecutive rows; lanes run over the row's 16-code
+// chunks (heads and, inside a head, neighbouring chunks), k and v alike.
+constexpr int kGatherRows = 4;
+
+template <bool BF16>
+__device__ __forceinline__ void gather_chunk(const int8_t *codes, float scale, void *out, int64_t elem, bool present) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (present) v = __ldg(reinterpret_cast<const uint4 *>(codes));
+  float y[16];
+  dequant16(v, scale, 0, y);
+  if constexpr (BF16) {
+    uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + elem);
+    o[0] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    o[1] = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]), pack_bf16x2(y[12], y[13]),
+                      pack_bf16x2(y[14], y[15]));
+  } else {
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + elem);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ KvGatherArgs a) {
+  pdl_launch_dependents();
+  pdl_wait_prerequisite();
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
+  const int cpd = a.c.d >> 4, cpr = a.c.heads * cpd;  // 16-code chunks of a head and of a row
+  int32_t b = -1, r0 = 0, r1 = 0, first = 0;
+  bool ok = false;
+  for (int64_t t = w * kGatherRows; t < min(a.rows, (w + 1) * kGatherRows); ++t) {
+    if (b < 0 || t >= r1) {
+      const int32_t *next = a.row_start + 1;
+      b = warp_count_le([&](int32_t i) { return static_cast<int64_t>(__ldg(next + i)); }, a.batch, t);
+      if (b >= a.batch) return;
+      r0 = __ldg(a.row_start + b);
+      r1 = __ldg(a.row_start + b + 1);
+      first = __ldg(a.first_pos + b);
+      ok = r0 >= 0 && r0 <= t && t < r1 && r1 <= a.rows && first >= 0 &&
+           static_cast<int64_t>(first) + (r1 - r0) <= static_cast<int64_t>(a.max_pages) << a.c.page_shift;
+      if (!ok) record_error(a.status, W8A8_ERR_BAD_SEQUENCE);
+    }
+    if (!ok) {
+      b = -1;
+      continue;
+    }
+    const int32_t pos = first + static_cast<int32_t>(t - r0);
+    const int32_t page = load_page(a.table + b * a.table_ld, pos >> a.c.page_shift, a.c.pages, a.status);
+    const int64_t block0 = static_cast<int64_t>(max(page, 0)) * a.c.heads;
+    for (int i = lane; i < cpr; i += 32) {
+      const int h = i / cpd, c = i - h * cpd;
+      const int64_t src = (((block0 + h) << a.c.page_shift) + (pos & (a.c.page - 1))) * a.c.d + 16 * c;
+      const int64_t dst = t * (static_cast<int64_t>(a.c.heads) * a.c.d) + 16 * i;
+      const bool here = page >= 0;
+      if (a.k_out) gather_chunk<BF16>(a.c.k + src, here ? __ldg(a.c.ks + block0 + h) : 0.0f, a.k_out, dst, here);
+      if (a.v_out) gather_chunk<BF16>(a.c.v + src, here ? __ldg(a.c.vs + block0 + h) : 0.0f, a.v_out, dst, here);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s) {
+  switch (a.c.d) {
+    case 64: return launch_append_t<64>(a, s);
+    case 96: return launch_append_t<96>(a, s);
+    case 128: return launch_append_t<128>(a, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_kv_gather(const KvGatherArgs &a, bool bf16_out, int num_sms, cudaStream_t s) {
+  (void)num_sms;
+  const int64_t warps = (a.rows + kGatherRows - 1) / kGatherRows;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = pdl_config((warps + kThreads / 32 - 1) / (kThreads / 32), s, &attr);
+  if (bf16_out) return cudaLaunchKernelEx(&cfg, gather_kernel<true>, a);
+  return cudaLaunchKernelEx(&cfg, gather_kernel<false>, a);
+}
+
+}  // namespace w8a8

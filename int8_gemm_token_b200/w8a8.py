@@ -56,6 +56,12 @@ _SIGNATURES = {
     "int8_mixed_decomp_gemm_tc": (_I32, [_P, _P, _P, _P, _P, _I32, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _I32,
                                          _P, _SZ, _P]),
     "int8_mixed_decomp_gemm_tc_workspace_size": (_SZ, [_I64, _I64, _I32]),
+    "w8a8_kv_append": (_I32, [_P, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I32, _I32, _P, _I64, _I64,
+                              _I32, _P, _P]),
+    "w8a8_kv_gather": (_I32, [_P, _P, _I64, _I32, _I32, _P, _P, _I64, _P, _P, _I32, _P]),
+    "w8a8_kv_attention": (_I32, [_P, _P, _I64, _P, _I64, _I64, _I32, _P, _P, _P, _SZ, _P]),
+    "w8a8_kv_attention_requant": (_I32, [_P, _P, _I64, _P, _I64, _I64, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
+    "w8a8_kv_attention_workspace_size": (_SZ, [_P, _P, _I64, _I32]),
     "w8a8_check_device_error": (_I32, [_P, _P]),
     "w8a8_debug_wait_timeout_selftest": (_I32, [ctypes.c_uint64, _P]),
 }
@@ -469,6 +475,225 @@ def int8_mixed_decomp_gemm_tc(Xq, S_x, Xo, idx, n_out, cap: int, Wq, s_w, W, bia
     when None) holds the padded side operands."""
     return _mixed("int8_mixed_decomp_gemm_tc", Xq, S_x, Xo, idx, n_out, cap, Wq, s_w, W, bias, out, out_dtype,
                   stream, workspace)
+
+
+# --------------------------------------------------------------------------
+# INT8 paged KV cache
+# --------------------------------------------------------------------------
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", _P), ("v_codes", _P), ("k_scale", _P), ("v_scale", _P), ("num_pages", _I64),
+                ("kv_heads", _I32), ("page_size", _I32), ("head_dim", _I32)]
+
+
+class _BatchStruct(ctypes.Structure):
+    _fields_ = [("page_table", _P), ("page_table_ld", _I64), ("seq_start", _P), ("kv_len", _P), ("batch", _I32),
+                ("max_pages", _I32), ("max_q_len", _I32), ("max_kv_len", _I32)]
+
+
+class _ScoresStruct(ctypes.Structure):
+    _fields_ = [("scale", _F), ("softcap", _F), ("slopes", _P), ("window", _I32), ("prefix_len", _P)]
+
+
+class PagedKVCache:
+    """An INT8 paged KV cache (w8a8_kv_cache): codes int8 [pages, kv_heads,
+    page_size, head_dim] and scales fp32 [pages, kv_heads], for keys and for
+    values. Checked once here; keeps the tensors alive. Their contents may
+    change between calls, the tensors may not be resized."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale):
+        if not isinstance(k_codes, torch.Tensor) or k_codes.dtype != torch.int8 or k_codes.dim() != 4:
+            raise ValueError("k_codes: expected an int8 tensor [pages, kv_heads, page_size, head_dim]")
+        shape = tuple(k_codes.shape)
+        _expect(k_codes, torch.int8, shape, "k_codes")
+        _expect(v_codes, torch.int8, shape, "v_codes")
+        _expect(k_scale, torch.float32, shape[:2], "k_scale")
+        _expect(v_scale, torch.float32, shape[:2], "v_scale")
+        if shape[2] not in (16, 32, 64, 128):
+            raise ValueError(f"k_codes: page size must be 16, 32, 64 or 128, got {shape[2]}")
+        if shape[3] not in (64, 96, 128):
+            raise ValueError(f"k_codes: head dim must be 64, 96 or 128, got {shape[3]}")
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = shape
+        self.device = k_codes.device
+        self._tensors = (k_codes, v_codes, k_scale, v_scale)
+        self._c = _CacheStruct(*(t.data_ptr() for t in self._tensors), *shape)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, device=None):
+        """A cache of zeroed pages."""
+        device = device or torch.device("cuda")
+        codes = [torch.zeros((num_pages, kv_heads, page_size, head_dim), dtype=torch.int8, device=device)
+                 for _ in range(2)]
+        scales = [torch.zeros((num_pages, kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *scales)
+
+
+class KVBatch:
+    """The sequences of a call (w8a8_kv_batch): page_table int32 [batch,
+    max_pages] (rows contiguous), seq_start int32 [batch + 1], kv_len int32
+    [batch], all on the device and read there, and the host's bounds on a
+    sequence's new tokens and length. Checked once here."""
+
+    def __init__(self, page_table, seq_start, kv_len, max_q_len: int, max_kv_len: int | None = None):
+        ld = _rows(page_table, torch.int32, "page_table")
+        batch, max_pages = page_table.shape
+        _vec(seq_start, torch.int32, batch + 1, "seq_start")
+        _vec(kv_len, torch.int32, batch, "kv_len")
+        self.page_table, self.seq_start, self.kv_len = page_table, seq_start, kv_len
+        self.max_q_len, self.max_kv_len = int(max_q_len), max_kv_len
+        self._tensors = (page_table, seq_start, kv_len)
+        self._max_pages = max_pages
+        self._c = _BatchStruct(page_table.data_ptr(), max(ld, max_pages), seq_start.data_ptr(), kv_len.data_ptr(),
+                               batch, max_pages, self.max_q_len, 0)
+        self._ref = ctypes.byref(self._c)
+
+    def _for(self, cache: PagedKVCache):
+        """The C struct, with the longest length the table can hold where the caller gave none."""
+        most = self._max_pages * cache.page_size
+        self._c.max_kv_len = most if self.max_kv_len is None else int(self.max_kv_len)
+        return self._ref
+
+
+def _heads3(t, heads, d, what: str, tokens=None):
+    """A bf16 tensor [tokens, heads, d] whose last axis is contiguous; returns
+    its strides between tokens and heads in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a tensor, got {type(t).__name__}")
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads) \
+            or (tokens is not None and t.shape[0] != tokens) or t.stride(2) != 1:
+        raise ValueError(f"{what}: expected bfloat16 [{'tokens' if tokens is None else tokens}, "
+                         f"{'heads' if heads is None else heads}, {d}] with a contiguous last axis, "
+                         f"got {t.dtype} {tuple(t.shape)} strides {tuple(t.stride())}")
+    st, sh = t.stride(0), t.stride(1)
+    # the stride of an axis of one (or no) element is never used; torch may report any value for it
+    return (st if t.shape[0] > 1 else 0), (sh if t.shape[1] > 1 else 0)
+
+
+def _kv_call(fn, dev, stream, *args):
+    """Call entry point `fn` with `dev` current, on the given stream or dev's current one."""
+    f = getattr(lib(), fn)
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            status = f(*args, _stream(stream))
+    else:
+        status = f(*args, _stream(stream))
+    _check(fn, status)
+
+
+def w8a8_kv_append(k, v, cache: PagedKVCache, batch: KVBatch, cos=None, sin=None, q=None, q_out=None,
+                   interleaved: bool = False, stream=None):
+    """Rotate (cos, sin fp32 [positions, rot_dim / 2]), quantize and store the
+    new tokens' keys and values; with q, rotate the queries into q_out (bf16
+    [tokens, q_heads, head_dim], allocated when None; returned)."""
+    d = cache.head_dim
+    kst, ksh = _heads3(k, cache.kv_heads, d, "k")
+    tokens = k.shape[0]
+    vst, vsh = _heads3(v, cache.kv_heads, d, "v", tokens)
+    rope_len = rot = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin: give both or neither")
+    if cos is not None:
+        if cos.dim() != 2:
+            raise ValueError(f"cos: expected [positions, rot_dim / 2], got {tuple(cos.shape)}")
+        _expect(cos, torch.float32, tuple(cos.shape), "cos")
+        _expect(sin, torch.float32, tuple(cos.shape), "sin")
+        rope_len, rot = cos.shape[0], 2 * cos.shape[1]
+    qst = qsh = hq = 0
+    if q is not None:
+        qst, qsh = _heads3(q, None, d, "q", tokens)
+        hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
+        _expect(q_out, torch.bfloat16, (tokens, hq, d), "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out: given without q")
+    _on_one_gpu(k, v, cos, sin, q, q_out, *cache._tensors, *batch._tensors)
+    _kv_call("w8a8_kv_append", cache.device, stream, cache._ref, batch._for(cache), tokens, _ptr(k), kst, ksh, _ptr(v),
+             vst, vsh, _ptr(cos), _ptr(sin), rope_len, rot, int(bool(interleaved)), _ptr(q), qst, qsh, hq, _ptr(q_out))
+    return q_out
+
+
+def w8a8_kv_gather(cache: PagedKVCache, page_table, first_pos, row_start, rows: int | None = None, k_out=None,
+                   v_out=None, out_dtype=torch.bfloat16, stream=None):
+    """Read positions first_pos[b] .. of each sequence back into rows
+    row_start[b] .. row_start[b + 1] of k_out and v_out [rows, kv_heads,
+    head_dim] (bf16 or fp32; both allocated for `rows` rows when neither is
+    given) -> (k_out, v_out)."""
+    ld = _rows(page_table, torch.int32, "page_table")
+    batch, max_pages = page_table.shape
+    _vec(first_pos, torch.int32, batch, "first_pos")
+    _vec(row_start, torch.int32, batch + 1, "row_start")
+    given = k_out if k_out is not None else v_out
+    if given is None:
+        if rows is None:
+            raise ValueError("rows: required where no output is given")
+        shape = (int(rows), cache.kv_heads, cache.head_dim)
+        k_out = _out(None, out_dtype, shape, cache.device, (torch.bfloat16, torch.float32), "k_out")
+        v_out = torch.empty_like(k_out)
+        given = k_out
+    shape = (given.shape[0] if rows is None else int(rows), cache.kv_heads, cache.head_dim)
+    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None:
+            _out(t, None, shape, None, (torch.bfloat16, torch.float32), what)
+            if t.dtype != given.dtype:
+                raise ValueError("v_out: expected the type of k_out")
+    _on_one_gpu(page_table, first_pos, row_start, k_out, v_out, *cache._tensors)
+    _kv_call("w8a8_kv_gather", cache.device, stream, cache._ref, _ptr(page_table), max(ld, max_pages), batch, max_pages,
+             _ptr(first_pos), _ptr(row_start), shape[0], _ptr(k_out), _ptr(v_out), _dt(given.dtype))
+    return k_out, v_out
+
+
+def w8a8_kv_attention_workspace_size(cache: PagedKVCache, batch: KVBatch, tokens: int, q_heads: int) -> int:
+    return int(lib().w8a8_kv_attention_workspace_size(cache._ref, batch._for(cache), tokens, q_heads))
+
+
+def _attention(fn, q, cache, batch, scale, softcap, window, slopes, prefix_len, out, out_dtype, extra, workspace, stream):
+    d = cache.head_dim
+    qst, qsh = _heads3(q, None, d, "q")
+    tokens, hq, _ = q.shape
+    _vec(slopes, torch.float32, hq, "slopes", optional=True)
+    _vec(prefix_len, torch.int32, batch.kv_len.shape[0], "prefix_len", optional=True)
+    if out is None:
+        out = torch.empty((tokens, hq, d), dtype=out_dtype, device=q.device)
+    _expect(out, out_dtype, (tokens, hq, d), "out")
+    _on_one_gpu(q, slopes, prefix_len, out, workspace, *extra, *cache._tensors, *batch._tensors)
+    bref = batch._for(cache)
+    if workspace is None:
+        if cache.device.index is not None and cache.device.index != torch.cuda.current_device():
+            with torch.cuda.device(cache.device):
+                need = int(lib().w8a8_kv_attention_workspace_size(cache._ref, bref, tokens, hq))
+        else:
+            need = int(lib().w8a8_kv_attention_workspace_size(cache._ref, bref, tokens, hq))
+        workspace, nbytes = _workspace(need, q.device, None)
+    else:
+        workspace, nbytes = _workspace(0, q.device, workspace)
+    sc = _ScoresStruct(d ** -0.5 if scale is None else float(scale), float(softcap), _ptr(slopes), int(window),
+                       _ptr(prefix_len))
+    _kv_call(fn, cache.device, stream, cache._ref, bref, tokens, _ptr(q), qst, qsh, hq, ctypes.byref(sc),
+             *(_ptr(t) for t in extra), _ptr(out), _ptr(workspace), nbytes)
+    return out
+
+
+def w8a8_kv_attention(q, cache: PagedKVCache, batch: KVBatch, scale: float | None = None, softcap: float = 0.0,
+                      window: int = 0, slopes=None, prefix_len=None, out=None, workspace=None, stream=None):
+    """Causal attention of bf16 q [tokens, q_heads, head_dim] over the cache ->
+    bf16 of the same shape (rows of no sequence are left as they are in a
+    given `out`). scale defaults to head_dim ** -0.5."""
+    return _attention("w8a8_kv_attention", q, cache, batch, scale, softcap, window, slopes, prefix_len, out,
+                      torch.bfloat16, (), workspace, stream)
+
+
+def w8a8_kv_attention_requant(q, cache: PagedKVCache, batch: KVBatch, r_out, Z_out, scale: float | None = None,
+                              softcap: float = 0.0, window: int = 0, slopes=None, prefix_len=None, out=None,
+                              workspace=None, stream=None):
+    """w8a8_kv_attention whose bf16 result is quantized at once with the output
+    projection's static r_out, Z_out: returns int8 [tokens, q_heads, head_dim]."""
+    _vec(r_out, torch.float32, 1, "r_out")
+    _vec(Z_out, torch.int32, 1, "Z_out")
+    return _attention("w8a8_kv_attention_requant", q, cache, batch, scale, softcap, window, slopes, prefix_len, out,
+                      torch.int8, (r_out, Z_out), workspace, stream)
 
 
 def w8a8_check_device_error(stream=None) -> int:
