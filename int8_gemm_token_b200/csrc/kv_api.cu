@@ -82,6 +82,12 @@ w8a8_status check_rows(const void *p, int64_t token_stride, int64_t head_stride,
   return W8A8_OK;
 }
 
+// Query rows of a kv head (new tokens x group) up to which the call takes the
+// kernel for few rows.
+constexpr int64_t kFewRows = 32;
+
+bool few_rows(const KvAttnArgs &a) { return static_cast<int64_t>(a.s.max_q) * a.group <= kFewRows; }
+
 // Cache, batch and heads of an attention call (what its workspace depends on).
 w8a8_status check_attention_shape(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch, int64_t tokens,
                                   int32_t q_heads, KvAttnArgs *a) {
@@ -91,7 +97,12 @@ w8a8_status check_attention_shape(const w8a8_kv_cache *cache, const w8a8_kv_batc
   if (q_heads % a->c.heads != 0 || q_heads / a->c.heads > kMaxGroup) return W8A8_ERR_UNSUPPORTED_SHAPE;
   a->q_heads = q_heads;
   a->group = q_heads / a->c.heads;
+  if (!few_rows(*a) && !kv_prefill_fits(*a)) return W8A8_ERR_UNSUPPORTED_SHAPE;
   return W8A8_OK;
+}
+
+size_t workspace_bytes_of(const KvAttnArgs &a, int sms) {
+  return few_rows(a) ? kv_decode_workspace_bytes(a, sms) : kv_prefill_workspace_bytes(a);
 }
 
 w8a8_status run_attention(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch, int64_t tokens, const void *q,
@@ -118,9 +129,10 @@ w8a8_status run_attention(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch
   a.z_out = z_out;
   int sms = 0;
   if (w8a8_status s = current_device_info(&sms, &a.status)) return s;
-  const size_t need = kv_decode_workspace_bytes(a, sms);
+  const size_t need = workspace_bytes_of(a, sms);
   if (need > 0 && (!workspace || workspace_bytes < need)) return W8A8_ERR_WORKSPACE;
-  return from_cuda(launch_kv_decode(a, workspace, sms, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return from_cuda(few_rows(a) ? launch_kv_decode(a, workspace, sms, st) : launch_kv_prefill(a, workspace, st));
 }
 
 }  // namespace
@@ -217,7 +229,7 @@ size_t w8a8_kv_attention_workspace_size(const w8a8_kv_cache *cache, const w8a8_k
   if (tokens == 0 || a.s.batch == 0 || a.s.max_q == 0) return 0;
   int sms = 0;
   if (current_device_info(&sms, &a.status) != W8A8_OK) return 0;
-  return kv_decode_workspace_bytes(a, sms);
+  return workspace_bytes_of(a, sms);
 }
 
 }  // extern "C"

@@ -65,4 +65,47 @@ __device__ __forceinline__ int quant_sym(float x, float r) {
   return min(max(rne_s32(__fmul_rn(x, r)), -127), 127);
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kGran = 16;  // a page holds whole granules of keys
+
+// Four int8 codes (bytes e0..e3 of w) as two bf16 pairs, exactly.
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t &p01, uint32_t &p23) {
+  const uint32_t a = __byte_perm(w, 0x43434343u, 0x4140), b = __byte_perm(w, 0x43434343u, 0x4342);
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p01) : "r"(a & 0xFF7FFF7Fu), "r"(a & 0xFF80FF80u));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p23) : "r"(b & 0xFF7FFF7Fu), "r"(b & 0xFF80FF80u));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The key tiles (of `tile` keys) that queries at positions first .. last - 1
+// see: [0, n1) for the prefix and [t0, ...) up to their own positions, both
+// cut at the sequence's n keys; tile number x of the walk is tile(x).
+struct TileWalk {
+  int n1, t0, count;
+  __device__ __forceinline__ int tile(int x) const { return x < n1 ? x : t0 + (x - n1); }
+};
+
+__device__ __forceinline__ TileWalk tile_walk(int tile, int prefix, int n, int first, int last, int window) {
+  TileWalk w;
+  w.n1 = (max(min(prefix, n), 0) + tile - 1) / tile;
+  w.t0 = max((window > 0 ? max(0, first - window + 1) : 0) / tile, w.n1);
+  w.count = w.n1 + max(0, (max(min(last, n), 0) + tile - 1) / tile - w.t0);
+  return w;
+}
+
+// Final value of one output element.
+__device__ __forceinline__ void store_out4(const KvAttnArgs &a, int64_t elem, const float (&y)[4]) {
+  const uint2 b = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+  if (!a.r_out) {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + elem) = b;
+    return;
+  }
+  const uint2 q = quant8_asym_sat(make_uint4(b.x, b.y, 0, 0), __ldg(a.r_out), __ldg(a.z_out));
+  *reinterpret_cast<uint32_t *>(static_cast<int8_t *>(a.out) + elem) = q.x;
+}
+
 }  // namespace w8a8

@@ -35,10 +35,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;    // keys of a warp's tile
-constexpr int kGran = 16;    // keys of an MMA tile; a page holds whole granules
 constexpr int kStages = 3;
 constexpr int kPagesAhead = 16;  // tiles whose pages and scales a warp holds, two granules each, one per lane
-constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Cfg {
@@ -68,13 +66,6 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Four int8 codes (bytes e0..e3 of w) as two bf16 pairs, exactly.
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t &p01, uint32_t &p23) {
-  const uint32_t a = __byte_perm(w, 0x43434343u, 0x4140), b = __byte_perm(w, 0x43434343u, 0x4342);
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p01) : "r"(a & 0xFF7FFF7Fu), "r"(a & 0xFF80FF80u));
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p23) : "r"(b & 0xFF7FFF7Fu), "r"(b & 0xFF80FF80u));
-}
-
 __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -86,12 +77,6 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -142,33 +127,6 @@ __device__ __forceinline__ void load_v_words(const uint8_t *v, int r, int g, uin
   }
 }
 
-// The key tiles a sequence's rows see: [0, n1) (prefix) and [t0, t1); tile
-// number x of the walk is x < n1 ? x : t0 + x - n1.
-struct TileWalk {
-  int n1, t0, count;
-  __device__ __forceinline__ int tile(int x) const { return x < n1 ? x : t0 + (x - n1); }
-};
-
-__device__ __forceinline__ TileWalk tile_walk(const KvAttnArgs &a, const KvSeq &seq, int32_t prefix) {
-  TileWalk w;
-  const int first = a.window > 0 ? max(0, max(seq.pos0(), 0) - a.window + 1) : 0;
-  w.n1 = (min(prefix, seq.n) + kTile - 1) / kTile;
-  w.t0 = max(first / kTile, w.n1);
-  w.count = w.n1 + max(0, (seq.n + kTile - 1) / kTile - w.t0);
-  return w;
-}
-
-// Final value of one output element.
-__device__ __forceinline__ void store_out4(const KvAttnArgs &a, int64_t elem, const float (&y)[4]) {
-  const uint2 b = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-  if (!a.r_out) {
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + elem) = b;
-    return;
-  }
-  const uint2 q = quant8_asym_sat(make_uint4(b.x, b.y, 0, 0), __ldg(a.r_out), __ldg(a.z_out));
-  *reinterpret_cast<uint32_t *>(static_cast<int8_t *>(a.out) + elem) = q.x;
-}
-
 // Partial results of a split: [sequence][kv head][row block][split] x (8 NT
 // rows x D sums, then 8 NT rows x (maximum, sum)).
 template <int D, int NT>
@@ -193,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int row0 = rb * ROWS;
   if (row0 >= rows) return;
   const int32_t prefix = a.prefix ? __ldg(a.prefix + b) : 0;
-  const TileWalk walk = tile_walk(a, seq, prefix);
+  const TileWalk walk = tile_walk(kTile, prefix, seq.n, max(seq.pos0(), 0), seq.n, a.window);
   const int per = (walk.count + splits - 1) / splits;
   const int x0 = min(walk.count, split * per), x1 = min(walk.count, x0 + per);
   const int32_t *table_row = a.s.table + b * a.s.table_ld;

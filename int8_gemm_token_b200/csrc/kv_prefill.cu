@@ -1,0 +1,575 @@
+// kv_prefill.cu -- attention of many new tokens over the INT8 paged KV cache,
+// on the 5th-generation tensor cores.
+//
+// What it computes: as kv_decode.cu (one pass over the keys with a running
+// maximum m and sum l), for chunks of prompts.
+//
+// How (sm_100a), two kernels:
+//   kv_expand_kernel writes the sequences' codes as bf16 (exactly) into dense
+//   [sequence][kv head][key][dim] matrices, 128-key tiles zero-padded, with
+//   the scales of each granule of 16 keys beside them. Every key tile is used
+//   by many query tiles; expanded once, it comes back through TMA in the
+//   layout the MMAs read and no query tile converts anything.
+//   kv_prefill_kernel: a block per 256 query rows of one kv head, in two
+//   tiles of 128 = floor(128 / group) tokens x group heads, so that grouped
+//   heads share their key tiles. Roles:
+//     warps 0-3, 4-7  softmax of tile A and of tile B, one thread per row:
+//                 S from TMEM (tcgen05.ld), maximum, 2^(s - m), row sum, and
+//                 the weights times v's scale back into TMEM as the bf16 A
+//                 operand of the second product (over S, which is dead by
+//                 then); at the end O / l to global memory;
+//     warp 8      TMA producer: 128-byte-swizzled 128 x 64 boxes of K and V
+//                 into a ring of key tiles;
+//     warp 9      MMA issuer: S = Q K^T (both K-major in shared memory) and
+//                 O += P V (P in TMEM, V as an MN-major operand, so V needs
+//                 no transpose). While one tile's softmax runs, the other
+//                 tile's products do.
+//   The page scales never touch the operands: k's multiplies the scores (a
+//   granule's maximum is scaled once, an element's factor is that of the
+//   fused multiply-add before 2^x), v's multiplies the weights.
+//   O is rescaled only when a row's maximum has grown by more than 2^8 since
+//   its last reference (weights then stay below 2^8 and nothing is lost in
+//   fp32); the softmax warps do it themselves between the products, since
+//   S_w(j) complete implies O_w(j - 1) complete.
+//   TMEM: S_A, S_B (128 columns each, fp32; P in their first 64), O_A, O_B.
+#include "kv_common.cuh"
+
+namespace w8a8 {
+
+namespace {
+
+constexpr int kKeys = 128;             // keys of a tile
+constexpr int kRows = 128;             // query rows of a tile = TMEM lanes
+constexpr int kBox = kKeys * 128;      // bytes of a 64-dim box of 128 rows
+constexpr int kSlots = 4;              // key tiles (K or V) in flight
+constexpr int kThreads = 320;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol = 256;        // S_A 0, S_B 128, O_A 256, O_B 384
+constexpr float kRescale = 8.0f;       // log2 of how far a maximum may outgrow its reference
+
+template <int D>
+struct PCfg {
+  static constexpr int kAtoms = D > 64 ? 2 : 1;       // 64-dim boxes of a row
+  static constexpr int kPitch = 64 * kAtoms;          // elements of an expanded row
+  static constexpr int kTile = kAtoms * kBox;         // bytes of a K, V or Q tile
+  static constexpr size_t kSmem = static_cast<size_t>(2 + kSlots) * kTile + 1024 + 256;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+int64_t expanded_len(int32_t max_kv) { return (static_cast<int64_t>(max_kv) + kKeys - 1) / kKeys * kKeys; }
+
+// ------------------------------------------------------------------ expansion
+// Block: 64 keys of one (kv head, sequence). Rows from the sequence's end to
+// the end of its last 128-key tile are zeros (they meet weights of 0, and
+// must not be NaN). A granule's scales: of its page; 0 past the end; -1 for a
+// page that does not exist.
+constexpr int kExpandKeys = 64;
+constexpr int kExpandThreads = 256;
+
+struct Expanded {
+  uint16_t *k, *v;      // [sequence][head][len][pitch]
+  float *ks, *vs;       // [sequence][head][len / 16]
+  int64_t len;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kExpandThreads) kv_expand_kernel(const __grid_constant__ KvAttnArgs a,
+                                                                   const __grid_constant__ Expanded x) {
+  constexpr int CH = D / 16, PITCH = PCfg<D>::kPitch;
+  __shared__ int32_t s_page[kExpandKeys / kGran];
+  pdl_launch_dependents();
+  pdl_wait_prerequisite();
+  const int b = blockIdx.z, h = blockIdx.y, key0 = blockIdx.x * kExpandKeys;
+  const KvSeq seq = load_seq(a.s, b, a.s.max_kv, a.status);
+  if (seq.q == 0 || key0 >= (seq.n + kKeys - 1) / kKeys * kKeys) return;
+  const int32_t prefix = a.prefix ? __ldg(a.prefix + b) : 0;
+  const TileWalk walk = tile_walk(kKeys, prefix, seq.n, max(seq.pos0(), 0), seq.n, a.window);
+  if (key0 >= walk.n1 * kKeys && key0 < walk.t0 * kKeys) return;  // no query sees this tile
+  const int64_t row0 = (static_cast<int64_t>(b) * a.c.heads + h) * x.len + key0;
+  if (threadIdx.x < kExpandKeys / kGran) {
+    const int key = key0 + threadIdx.x * kGran;
+    int32_t page = -1;
+    float ks = 0.0f, vs = 0.0f;
+    if (key < seq.n) {
+      page = load_page(a.s.table + b * a.s.table_ld, key >> a.c.page_shift, a.c.pages, a.status);
+      ks = page < 0 ? -1.0f : __ldg(a.c.ks + static_cast<int64_t>(page) * a.c.heads + h);
+      vs = page < 0 ? 0.0f : __ldg(a.c.vs + static_cast<int64_t>(page) * a.c.heads + h);
+    }
+    s_page[threadIdx.x] = page;
+    const int64_t at = row0 / kGran + threadIdx.x;
+    x.ks[at] = ks;
+    x.vs[at] = vs;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kExpandKeys * CH; i += kExpandThreads) {
+    const int r = i / CH, c = i - r * CH;
+    const int key = key0 + r;
+    const int32_t page = s_page[r / kGran];
+    uint4 kv[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (page >= 0 && key < seq.n) {
+      const int64_t src =
+          (((static_cast<int64_t>(page) * a.c.heads + h) << a.c.page_shift) + (key & (a.c.page - 1))) * D + 16 * c;
+      kv[0] = __ldg(reinterpret_cast<const uint4 *>(a.c.k + src));
+      kv[1] = __ldg(reinterpret_cast<const uint4 *>(a.c.v + src));
+    }
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const uint32_t w[4] = {kv[z].x, kv[z].y, kv[z].z, kv[z].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) codes_to_bf16(w[e], o[2 * e], o[2 * e + 1]);
+      uint4 *dst = reinterpret_cast<uint4 *>((z ? x.v : x.k) + (row0 + r) * PITCH + 16 * c);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ attention
+__device__ __forceinline__ void fma2(float &x0, float &x1, float c, float d) {  // x = x c + d, two at a time
+  asm("{\n\t.reg .b64 a, b, e;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmov.b64 e, {%3, %3};\n\t"
+      "fma.rn.f32x2 a, a, b, e;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float &x0, float &x1, float y0, float y1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(y0), "f"(y1));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_prefill_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ KvAttnArgs a, const __grid_constant__ Expanded x, int64_t slots_total,
+                      uint64_t limit_ns) {
+  using C = PCfg<D>;
+  constexpr int KS = D / 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sQ = base;                    // two tiles
+  uint8_t *sKV = base + 2 * C::kTile;    // ring of key tiles
+  uint64_t *full_bar = reinterpret_cast<uint64_t *>(sKV + kSlots * C::kTile);
+  uint64_t *empty_bar = full_bar + kSlots;
+  uint64_t *s_bar = empty_bar + kSlots;  // [2] scores of a tile are in TMEM
+  uint64_t *p_bar = s_bar + 2;           // [2] its weights are (one arrival per softmax warp)
+  uint64_t *o_bar = p_bar + 2;           // [2] its output is final
+  uint64_t *drain_bar = o_bar + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain_bar + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    if (x.len > 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&s_bar[w], 1);
+      mbar_init(&p_bar[w], 4);
+      mbar_init(&o_bar[w], 1);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_launch_dependents();
+  pdl_wait_prerequisite();
+
+  // The block's sequence and query tiles. Slot f(b) = seq_start[b] / T + b
+  // leaves sequence b room for its ceil(q / T) blocks of T tokens. Later
+  // tokens see more keys, so slots are walked from the last.
+  const int tpt = kRows / a.group, T = 2 * tpt;
+  const int64_t slot = slots_total - 1 - blockIdx.x / a.c.heads;
+  const int h = static_cast<int>(blockIdx.x % a.c.heads);
+  const auto f = [&](int32_t i) { return static_cast<int64_t>(__ldg(a.s.seq_start + i) / T) + i; };
+  const int32_t b = warp_count_le(f, a.s.batch, slot) - 1;
+  KvSeq seq = {0, 0, 0};
+  if (b >= 0) seq = load_seq(a.s, b, a.s.max_kv, a.status);
+  const int64_t tile = b >= 0 ? slot - f(b) : 0;
+  const int32_t prefix = a.prefix && b >= 0 ? __ldg(a.prefix + b) : 0;
+  const bool work = tile * T < seq.q;
+  const int tok0 = work ? static_cast<int>(tile) * T : 0;  // the block's first token in its sequence
+  const int first_pos = max(seq.pos0() + tok0, 0);
+  // Tokens of tile A (t = 0) or B, and the key tiles it walks. Both walk from
+  // the block's first key, so one walk is a prefix of the other.
+  const auto toks_of = [&](int t) { return work ? max(0, min(tpt, seq.q - tok0 - t * tpt)) : 0; };
+  const auto count_of = [&](int t) {
+    const int last = seq.pos0() + tok0 + t * tpt + toks_of(t);  // one past its last position
+    return toks_of(t) > 0 && last > 0 ? tile_walk(kKeys, prefix, seq.n, first_pos, last, a.window).count : 0;
+  };
+  const TileWalk walk = tile_walk(kKeys, prefix, seq.n, first_pos, seq.n, a.window);
+  const int count_a = count_of(0), count_b = count_of(1), most = max(count_a, count_b);
+  const int64_t krow = (static_cast<int64_t>(max(b, 0)) * a.c.heads + h) * x.len;
+
+  // Q rows into shared memory, swizzled as TMA would; zeros where there is no row
+  const int w = warp >> 2;  // softmax tile of warps 0..7
+  const int row = threadIdx.x & (kRows - 1);
+  const int tok = row / a.group, hq = h * a.group + (row - tok * a.group);
+  const int my_tok0 = tok0 + w * tpt, my_toks = w < 2 ? toks_of(w) : 0;
+  const bool real = tok < my_toks;
+  if (w < 2 && work) {
+    uint8_t *q_row = sQ + w * C::kTile + row * 128;
+    const uint16_t *src = a.q.p + (seq.row0 + my_tok0 + tok) * a.q.token_stride + hq * a.q.head_stride;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (real) v = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+      *reinterpret_cast<uint4 *>(q_row + (c >> 3) * kBox + (((c & 7) ^ (row & 7)) << 4)) = v;
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 8) {
+    if (lane == 0 && most > 0) {
+      // ------------------------------------------------ TMA producer: K(0), V(0), K(1), V(1), ...
+      bool ok = true;
+      uint32_t issued = 0, parity = 0;
+      for (int i = 0; i < 2 * most; ++i) {
+        const int s = i % kSlots;
+        const uint32_t ph = static_cast<uint32_t>(i / kSlots) & 1u;
+        if (!mbar_wait_bounded(&empty_bar[s], ph ^ 1u, abort_flag, limit_ns)) {
+          ok = false;
+          break;
+        }
+        const int32_t y = static_cast<int32_t>(krow + walk.tile(i >> 1) * kKeys);
+        const CUtensorMap *map = (i & 1) ? &tmV : &tmK;
+        mbar_arrive_expect_tx(&full_bar[s], C::kTile);
+#pragma unroll
+        for (int c = 0; c < C::kAtoms; ++c) tma_load_2d(map, &full_bar[s], sKV + s * C::kTile + c * kBox, 64 * c, y);
+        issued |= 1u << s;
+        parity = (parity & ~(1u << s)) | (ph << s);
+      }
+      if (!ok) {
+        record_error(a.status, W8A8_ERR_DEVICE_TIMEOUT);
+        *abort_flag = 1;
+        for (int s = 0; s < kSlots; ++s)
+          if (issued & (1u << s)) mbar_wait_bounded(&full_bar[s], (parity >> s) & 1u, nullptr, limit_ns / 16 + 1);
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0 && most > 0) {
+      // ------------------------------------------------ MMA issuer
+      constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kKeys), kIdescO = idesc_bf16_f32_bt(kRows, D);
+      bool ok = true;
+      const auto wait_full = [&](int i) {
+        if (!mbar_wait_bounded(&full_bar[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u, abort_flag, limit_ns))
+          ok = false;
+        tc_fence_after();
+      };
+      const auto scores = [&](int t, int i) {  // S_t = Q_t K^T with the key tile of ring item i
+        const uint32_t qa = smem_addr(sQ + t * C::kTile), ka = smem_addr(sKV + (i % kSlots) * C::kTile);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t off = (k >> 2) * kBox + (k & 3) * 32;
+          mma_bf16(tmem + t * kKeys, smem_desc_k_sw128(qa + off), smem_desc_k_sw128(ka + off), kIdescS, k != 0);
+        }
+        mma_commit(&s_bar[t]);
+      };
+      wait_full(0);
+      if (ok) {
+        for (int t = 0; t < 2; ++t)
+          if ((t ? count_b : count_a) > 0) scores(t, 0);
+        mma_commit(&empty_bar[0]);
+      }
+      for (int j = 0; j < most && ok; ++j) {
+        const int iv = 2 * j + 1, ik = iv + 1;
+        wait_full(iv);
+        if (ok && j + 1 < most) wait_full(ik);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int count = t ? count_b : count_a;
+          if (!ok || j >= count) continue;
+          if (!mbar_wait_bounded(&p_bar[t], static_cast<uint32_t>(j) & 1u, abort_flag, limit_ns)) {
+            ok = false;
+            continue;
+          }
+          tc_fence_after();
+          const uint32_t va = smem_addr(sKV + (iv % kSlots) * C::kTile);
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_bf16_ta(tmem + kOCol + t * kKeys, tmem + t * kKeys + 8 * k, smem_desc_mn_sw128(va + 2048 * k, kBox),
+                        kIdescO, (j | k) != 0);
+          // the next scores overwrite the weights just read: the tensor core works in order
+          if (j + 1 < count)
+            scores(t, ik);
+          else
+            mma_commit(&o_bar[t]);
+        }
+        if (ok) {
+          mma_commit(&empty_bar[iv % kSlots]);
+          if (j + 1 < most) mma_commit(&empty_bar[ik % kSlots]);
+        }
+      }
+      if (!ok) {
+        record_error(a.status, W8A8_ERR_DEVICE_TIMEOUT);
+        *abort_flag = 1;
+        mma_commit(drain_bar);  // MMAs in flight finish before TMEM is freed
+        mbar_wait_bounded(drain_bar, 0, nullptr, limit_ns / 16 + 1);
+      }
+    }
+  } else if (work) {
+    // -------------------------------------------------- softmax
+    const int count = w ? count_b : count_a;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + static_cast<uint32_t>(w * kKeys);
+    const uint32_t t_o = t_s + kOCol;
+    const int pos = real ? seq.pos0() + my_tok0 + tok : -1;
+    const int pos_min = seq.pos0() + my_tok0, pos_max = pos_min + my_toks - 1;
+    const bool cap = a.softcap > 0.0f;
+    const float mul = cap ? a.scale / a.softcap : a.scale * kLog2e;
+    const float cap2 = a.softcap * kLog2e;
+    const float slope = a.slopes && real ? __ldg(a.slopes + hq) * kLog2e : 0.0f;
+    const bool plain = !cap && !a.slopes && a.scale >= 0.0f;  // a granule's largest score is its largest product
+    float m = -INFINITY, l = 0.0f;
+    bool ok = true;
+    float4 kc4[2], vc4[2];
+    const float *ks = x.ks + krow / kGran, *vs = x.vs + krow / kGran;
+    const auto fetch_scales = [&](int j) {
+      const int64_t at = static_cast<int64_t>(walk.tile(j)) * (kKeys / kGran);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        kc4[e] = *reinterpret_cast<const float4 *>(ks + at + 4 * e);
+        vc4[e] = *reinterpret_cast<const float4 *>(vs + at + 4 * e);
+      }
+    };
+    if (count > 0) fetch_scales(0);
+    for (int j = 0; j < count; ++j) {
+      float kc[8] = {kc4[0].x, kc4[0].y, kc4[0].z, kc4[0].w, kc4[1].x, kc4[1].y, kc4[1].z, kc4[1].w};
+      const float vc[8] = {vc4[0].x, vc4[0].y, vc4[0].z, vc4[0].w, vc4[1].x, vc4[1].y, vc4[1].z, vc4[1].w};
+      if (j + 1 < count) fetch_scales(j + 1);
+      const int key0 = walk.tile(j) * kKeys;
+      bool whole = key0 + kKeys - 1 <= pos_min && (a.window == 0 || key0 > pos_max - a.window);
+#pragma unroll
+      for (int g = 0; g < 8; ++g) whole = whole && kc[g] != -1.0f;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&s_bar[w], static_cast<uint32_t>(j) & 1u, abort_flag, limit_ns))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float top = -INFINITY;
+      if (whole && plain) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t s[32];
+          tmem_ld_32x32b_x32(t_s + 32 * c, s);
+          tmem_ld_wait();
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float v = __uint_as_float(s[16 * g]);
+#pragma unroll
+            for (int e = 1; e < 16; ++e) v = fmaxf(v, __uint_as_float(s[16 * g + e]));
+            top = fmaxf(top, v * (kc[2 * c + g] * mul));
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < 8; ++g) kc[g] *= mul;
+      } else {  // element by element; the finished scores go back to TMEM
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t s[32];
+          tmem_ld_32x32b_x32(t_s + 32 * c, s);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float k1 = kc[2 * c + (e >> 4)];
+            float v = __uint_as_float(s[e]) * (k1 * mul);
+            if (cap) v = cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(v * (2.0f * kLog2e)));
+            const int key = key0 + 32 * c + e;
+            v += slope * static_cast<float>(key - pos);
+            const bool seen = k1 != -1.0f && key < seq.n && pos >= 0 &&
+                              ((key <= pos && (a.window == 0 || pos - key < a.window)) || key < prefix);
+            v = seen ? v : -INFINITY;
+            top = fmaxf(top, v);
+            s[e] = __float_as_uint(v);
+          }
+          tmem_st_32x32b_x32(t_s + 32 * c, s);
+        }
+        tmem_st_wait();
+#pragma unroll
+        for (int g = 0; g < 8; ++g) kc[g] = 1.0f;
+      }
+      const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        const float fr = grow ? ex2(m - top) : 1.0f;
+        if (grow) m = top;
+        l *= fr;
+        if (j > 0) {  // O_w(j - 1) is complete, O_w(j) waits for this warp
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(t_o + 32 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fr);
+            tmem_st_32x32b_x32(t_o + 32 * c, o);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.0f : -m;
+      float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+      for (int c2 = 0; c2 < 2; ++c2) {
+        uint32_t p[32];
+#pragma unroll
+        for (int c1 = 0; c1 < 2; ++c1) {
+          const int c = 2 * c2 + c1;
+          uint32_t s[32];
+          tmem_ld_32x32b_x32(t_s + 32 * c, s);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const int g = 2 * c + (e >> 4);
+            float s0 = __uint_as_float(s[e]), s1 = __uint_as_float(s[e + 1]);
+            fma2(s0, s1, kc[g], ref);
+            float p0 = ex2(s0), p1 = ex2(s1);
+            add2(l0, l1, p0, p1);
+            if (whole) {
+              mul_f32x2(p0, p1, vc[g], p0, p1);
+            } else {  // (not 0 times the scale of a page that no row sees, which may be anything)
+              p0 = p0 > 0.0f ? p0 * vc[g] : 0.0f;
+              p1 = p1 > 0.0f ? p1 * vc[g] : 0.0f;
+            }
+            p[16 * c1 + (e >> 1)] = pack_bf16x2(p0, p1);
+          }
+        }
+        tmem_st_32x32b_x32(t_s + 32 * c2, p);  // columns whose scores have been read
+      }
+      l += l0 + l1;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_bar[w]);
+    }
+    if (ok && count > 0)
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&o_bar[w], 0, abort_flag, limit_ns));
+    if (!ok) {
+      if (lane == 0) {
+        record_error(a.status, W8A8_ERR_DEVICE_TIMEOUT);
+        *abort_flag = 1;
+      }
+    } else {
+      tc_fence_after();
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const int64_t elem = (static_cast<int64_t>(seq.row0 + my_tok0 + tok) * a.q_heads + hq) * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0;
+        if (count > 0) {
+          tmem_ld_32x32b_x32(t_o + 32 * c, o);
+          tmem_ld_wait();
+        }
+        if (real) {
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            y[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          if (!a.r_out) {
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + elem + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          } else {
+            const float r = __ldg(a.r_out);
+            const int z = __ldg(a.z_out);
+            uint2 *dst = reinterpret_cast<uint2 *>(static_cast<int8_t *>(a.out) + elem + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = quant8_asym_sat(make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]), r, z);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();  // lanes of the producer and MMA warps reconverge before the CTA barrier
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+Expanded expanded_of(const KvAttnArgs &a, void *workspace) {
+  Expanded x;
+  x.len = expanded_len(a.s.max_kv);
+  const int64_t keys = static_cast<int64_t>(a.s.batch) * a.c.heads * x.len;
+  const int64_t pitch = a.c.d > 64 ? 128 : 64;
+  x.k = static_cast<uint16_t *>(workspace);
+  x.v = x.k + keys * pitch;
+  x.ks = reinterpret_cast<float *>(x.v + keys * pitch);
+  x.vs = x.ks + keys / kGran;
+  return x;
+}
+
+template <int D>
+cudaError_t launch_t(const KvAttnArgs &a, void *workspace, cudaStream_t s) {
+  using C = PCfg<D>;
+  const Expanded x = expanded_of(a, workspace);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = s;
+  alignas(64) CUtensorMap tmK = {}, tmV = {};  // not used where no sequence has a key
+  const uint64_t rows = static_cast<uint64_t>(a.s.batch) * a.c.heads * x.len;
+  if (rows > 0) {
+    if (!encode_tmap_2d(&tmK, x.k, TmapType::kBF16, C::kPitch, rows, C::kPitch * 2, 64, kKeys, true) ||
+        !encode_tmap_2d(&tmV, x.v, TmapType::kBF16, C::kPitch, rows, C::kPitch * 2, 64, kKeys, true))
+      return cudaErrorInvalidValue;
+    cfg.gridDim = dim3(static_cast<unsigned>(x.len / kExpandKeys), a.c.heads, a.s.batch);
+    cfg.blockDim = dim3(kExpandThreads);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kv_expand_kernel<D>, a, x);
+    if (e != cudaSuccess) return e;
+  }
+  cudaError_t e = ensure_kernel_smem<kv_prefill_kernel<D>>(static_cast<int>(C::kSmem), false);
+  if (e != cudaSuccess) return e;
+  const int T = 2 * (kRows / a.group);
+  const int64_t slots = a.s.tokens / T + a.s.batch;
+  cfg.gridDim = dim3(static_cast<unsigned>(slots * a.c.heads));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  return cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D>, tmK, tmV, a, x, slots, kWaitLimitNs);
+}
+
+}  // namespace
+
+bool kv_prefill_fits(const KvAttnArgs &a) {
+  // rows of the expanded matrices are int32 tensor-map coordinates, slots x heads a grid
+  const int64_t rows = static_cast<int64_t>(a.s.batch) * a.c.heads * expanded_len(a.s.max_kv);
+  const int64_t blocks = (a.s.tokens / (2 * (kRows / a.group)) + a.s.batch) * a.c.heads;
+  return rows <= INT32_MAX && blocks <= INT32_MAX;
+}
+
+size_t kv_prefill_workspace_bytes(const KvAttnArgs &a) {
+  const size_t keys = static_cast<size_t>(a.s.batch) * a.c.heads * expanded_len(a.s.max_kv);
+  return keys * ((a.c.d > 64 ? 128 : 64) * 2 * sizeof(uint16_t)) + keys / kGran * 2 * sizeof(float);
+}
+
+cudaError_t launch_kv_prefill(const KvAttnArgs &a, void *workspace, cudaStream_t s) {
+  switch (a.c.d) {
+    case 64: return launch_t<64>(a, workspace, s);
+    case 96: return launch_t<96>(a, workspace, s);
+    case 128: return launch_t<128>(a, workspace, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace w8a8
