@@ -257,6 +257,15 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -272,21 +281,6 @@ __device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t smem_byte_addr) {
   d |= static_cast<uint64_t>(1024 >> 4) << 32;                    // stride byte offset
   d |= static_cast<uint64_t>(1) << 46;                            // descriptor version
   d |= static_cast<uint64_t>(2) << 61;                            // SWIZZLE_128B
-  return d;
-}
-
-// Shared-memory matrix descriptor of an operand whose contraction axis is the
-// slow one (MN-major), in the layout TMA's SWIZZLE_128B writes for a box of
-// 64 16-bit columns: a row of 128 bytes per contraction index, 8 rows to a
-// swizzle atom of 1024 bytes (stride byte offset), further groups of 64
-// columns `group_bytes` away (leading byte offset).
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t smem_byte_addr, uint32_t group_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_byte_addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(group_bytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
 
@@ -314,25 +308,55 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 // idesc_bf16_f32 with an MN-major B.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32_bt(int M, int N) { return idesc_bf16_f32(M, N) | (1u << 16); }
 
-// D[tmem] (+)= A[smem] * B[smem], bf16 operands, fp32 accumulator (K = 16 an instruction).
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// One lane of a converged warp (the same one every time), for instructions
+// that one thread issues from warp-uniform operands.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// The two halves of a 128-byte-swizzled matrix descriptor. Upper: stride byte
+// offset, version, swizzle, the same for both majors. Lower: the start
+// address and the leading byte offset in units of 16 bytes, so a step of n
+// bytes inside an operand adds n / 16 to it.
+//   K-major: as smem_desc_k_sw128.
+//   MN-major (the contraction axis is the slow one), in the layout TMA's
+//   SWIZZLE_128B writes for a box of 64 16-bit columns: a row of 128 bytes
+//   per contraction index, 8 rows to a swizzle atom of 1024 bytes (stride byte
+//   offset), further groups of 64 columns `group_bytes` away (leading byte
+//   offset).
+constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo_k_sw128(uint32_t smem_byte_addr) {
+  return ((smem_byte_addr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+__device__ __forceinline__ uint32_t desc_lo_mn_sw128(uint32_t smem_byte_addr, uint32_t group_bytes) {
+  return ((smem_byte_addr & 0x3FFFFu) >> 4) | ((group_bytes >> 4) << 16);
+}
+
+// D[tmem] (+)= A[smem] * B[smem], bf16 operands, fp32 accumulator (K = 16 an
+// instruction), given the lower halves of the descriptors.
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128)
       : "memory");
 }
 
 // The same with A in TMEM: lane = row, two consecutive contraction elements to a 32-bit column.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128)
       : "memory");
 }
 

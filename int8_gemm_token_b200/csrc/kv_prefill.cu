@@ -32,6 +32,8 @@
 //   fp32); the softmax warps do it themselves between the products, since
 //   S_w(j) complete implies O_w(j - 1) complete.
 //   TMEM: S_A, S_B (128 columns each, fp32; P in their first 64), O_A, O_B.
+#include <type_traits>
+
 #include "kv_common.cuh"
 
 namespace w8a8 {
@@ -42,7 +44,12 @@ constexpr int kKeys = 128;             // keys of a tile
 constexpr int kRows = 128;             // query rows of a tile = TMEM lanes
 constexpr int kBox = kKeys * 128;      // bytes of a 64-dim box of 128 rows
 constexpr int kSlots = 4;              // key tiles (K or V) in flight
-constexpr int kThreads = 320;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // softmax, producer, MMA, two idle
+// Registers a thread: 168 at launch (65536 / 384); a softmax thread holds a
+// whole row of 128 scores and wants more, the others few.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + 32 * 4 * kOtherRegs <= kThreads * 168, "register split");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;        // S_A 0, S_B 128, O_A 256, O_B 384
 constexpr float kRescale = 8.0f;       // log2 of how far a maximum may outgrow its reference
@@ -132,6 +139,23 @@ __device__ __forceinline__ void fma2(float &x0, float &x1, float c, float d) {  
       : "+f"(x0), "+f"(x1)
       : "f"(c), "f"(d));
 }
+using Yes = std::true_type;
+using No = std::false_type;
+
+__device__ __forceinline__ void axpy2(float &y0, float &y1, float x0, float x1, float c) {  // y += x c, two at a time
+  asm("{\n\t.reg .b64 a, b, e;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 e, {%0, %1};\n\t"
+      "fma.rn.f32x2 e, a, b, e;\n\tmov.b64 {%0, %1}, e;\n\t}"
+      : "+f"(y0), "+f"(y1)
+      : "f"(x0), "f"(x1), "f"(c));
+}
+// Bits 0 .. n - 1 of a granule (n below 0 or past 16 taken as 0 or 16).
+__device__ __forceinline__ uint32_t bits_below(int n) { return (1u << min(max(n, 0), 16)) - 1u; }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void add2(float &x0, float &x1, float y0, float y1) {
   asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\t"
       "mov.b64 {%0, %1}, a;\n\t}"
@@ -149,12 +173,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sQ = base;                    // two tiles
-  uint8_t *sKV = base + 2 * C::kTile;    // ring of key tiles
+  uint8_t *sKV = base + 2 * C::kTile;   // ring of key tiles
   uint64_t *full_bar = reinterpret_cast<uint64_t *>(sKV + kSlots * C::kTile);
   uint64_t *empty_bar = full_bar + kSlots;
-  uint64_t *s_bar = empty_bar + kSlots;  // [2] scores of a tile are in TMEM
-  uint64_t *p_bar = s_bar + 2;           // [2] its weights are (one arrival per softmax warp)
-  uint64_t *o_bar = p_bar + 2;           // [2] its output is final
+  uint64_t *s_bar = empty_bar + kSlots;  // [tile] scores are in TMEM
+  uint64_t *p_bar = s_bar + 2;           // [tile][half of the keys] weights are (one arrival per softmax warp)
+  uint64_t *o_bar = p_bar + 4;           // [tile] the output is final
   uint64_t *drain_bar = o_bar + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain_bar + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -169,16 +193,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&s_bar[w], 1);
-      mbar_init(&p_bar[w], 4);
-      mbar_init(&o_bar[w], 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_bar[t], 1);
+      mbar_init(&p_bar[2 * t], kSoftmaxWarps / 2);
+      mbar_init(&p_bar[2 * t + 1], kSoftmaxWarps / 2);
+      mbar_init(&o_bar[t], 1);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == 9) {
+  static_assert((2 * kSlots + 9) * 8 + 8 <= 256, "barriers and flags fit their reserve");
+  if (warp == kSoftmaxWarps + 1) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
@@ -212,19 +238,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t krow = (static_cast<int64_t>(max(b, 0)) * a.c.heads + h) * x.len;
 
   // Q rows into shared memory, swizzled as TMA would; zeros where there is no row
-  const int w = warp >> 2;  // softmax tile of warps 0..7
+  const int w = (warp >> 2) & 1;  // query tile of a softmax warp
+  const bool softmax = warp < kSoftmaxWarps;
   const int row = threadIdx.x & (kRows - 1);
   const int tok = row / a.group, hq = h * a.group + (row - tok * a.group);
-  const int my_tok0 = tok0 + w * tpt, my_toks = w < 2 ? toks_of(w) : 0;
+  const int my_tok0 = tok0 + w * tpt, my_toks = softmax ? toks_of(w) : 0;
   const bool real = tok < my_toks;
-  if (w < 2 && work) {
-    uint8_t *q_row = sQ + w * C::kTile + row * 128;
-    const uint16_t *src = a.q.p + (seq.row0 + my_tok0 + tok) * a.q.token_stride + hq * a.q.head_stride;
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
+  if (softmax && work) {
+    // each warp its 32 rows, the chunks of a row by neighbouring lanes (whole
+    // sectors; a lane per row would touch 32 far rows with every load)
+#pragma unroll 4
+    for (int i = lane; i < 32 * (D / 8); i += 32) {
+      const int r = (warp & 3) * 32 + i / (D / 8), c = i % (D / 8);
+      const int r_tok = r / a.group;
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (real) v = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-      *reinterpret_cast<uint4 *>(q_row + (c >> 3) * kBox + (((c & 7) ^ (row & 7)) << 4)) = v;
+      if (r_tok < my_toks)
+        v = __ldg(reinterpret_cast<const uint4 *>(a.q.p + (seq.row0 + my_tok0 + r_tok) * a.q.token_stride +
+                                                  (h * a.group + (r - r_tok * a.group)) * a.q.head_stride) + c);
+      *reinterpret_cast<uint4 *>(sQ + w * C::kTile + r * 128 + (c >> 3) * kBox + (((c & 7) ^ (r & 7)) << 4)) = v;
     }
     fence_proxy_async_smem();
   }
@@ -233,100 +264,124 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 8) {
-    if (lane == 0 && most > 0) {
-      // ------------------------------------------------ TMA producer: K(0), V(0), K(1), V(1), ...
+  // Ring items in the order the MMAs use them: K(0), then V(j), K(j + 1) for j = 0, 1, ...
+  if (warp >= kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kSoftmaxWarps && lane == 0 && most > 0) {
+      // ------------------------------------------------ TMA producer
       bool ok = true;
-      uint32_t issued = 0, parity = 0;
-      for (int i = 0; i < 2 * most; ++i) {
+      int i = 0;
+      const auto load = [&](const CUtensorMap *map, int j) {
+        if (!ok) return;
         const int s = i % kSlots;
-        const uint32_t ph = static_cast<uint32_t>(i / kSlots) & 1u;
-        if (!mbar_wait_bounded(&empty_bar[s], ph ^ 1u, abort_flag, limit_ns)) {
+        if (!mbar_wait_bounded(&empty_bar[s], (static_cast<uint32_t>(i / kSlots) & 1u) ^ 1u, abort_flag, limit_ns)) {
           ok = false;
-          break;
+          return;
         }
-        const int32_t y = static_cast<int32_t>(krow + walk.tile(i >> 1) * kKeys);
-        const CUtensorMap *map = (i & 1) ? &tmV : &tmK;
+        const int32_t y = static_cast<int32_t>(krow + walk.tile(j) * kKeys);
         mbar_arrive_expect_tx(&full_bar[s], C::kTile);
 #pragma unroll
         for (int c = 0; c < C::kAtoms; ++c) tma_load_2d(map, &full_bar[s], sKV + s * C::kTile + c * kBox, 64 * c, y);
-        issued |= 1u << s;
-        parity = (parity & ~(1u << s)) | (ph << s);
+        ++i;
+      };
+      load(&tmK, 0);
+      for (int j = 0; j < most && ok; ++j) {
+        load(&tmV, j);
+        if (j + 1 < most) load(&tmK, j + 1);
       }
       if (!ok) {
         record_error(a.status, W8A8_ERR_DEVICE_TIMEOUT);
         *abort_flag = 1;
-        for (int s = 0; s < kSlots; ++s)
-          if (issued & (1u << s)) mbar_wait_bounded(&full_bar[s], (parity >> s) & 1u, nullptr, limit_ns / 16 + 1);
+        for (int n = max(0, i - kSlots); n < i; ++n)  // copies in flight land before the block leaves
+          mbar_wait_bounded(&full_bar[n % kSlots], static_cast<uint32_t>(n / kSlots) & 1u, nullptr, limit_ns / 16 + 1);
       }
     }
-  } else if (warp == 9) {
-    if (lane == 0 && most > 0) {
+    if (warp == kSoftmaxWarps + 1 && most > 0) {
       // ------------------------------------------------ MMA issuer
+      // The whole warp walks the loop, so that every operand is warp-uniform,
+      // and one elected lane issues.
       constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kKeys), kIdescO = idesc_bf16_f32_bt(kRows, D);
+      const uint32_t q_lo = desc_lo_k_sw128(smem_addr(sQ)), k_lo = desc_lo_k_sw128(smem_addr(sKV)),
+                     v_lo = desc_lo_mn_sw128(smem_addr(sKV), kBox);
       bool ok = true;
-      const auto wait_full = [&](int i) {
-        if (!mbar_wait_bounded(&full_bar[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u, abort_flag, limit_ns))
-          ok = false;
+      int i = 0;  // next ring item
+      const auto wait_item = [&]() {
+        const int s = i % kSlots;
+        if (ok)
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full_bar[s], static_cast<uint32_t>(i / kSlots) & 1u, abort_flag,
+                                                         limit_ns));
         tc_fence_after();
+        ++i;
+        return s;
       };
-      const auto scores = [&](int t, int i) {  // S_t = Q_t K^T with the key tile of ring item i
-        const uint32_t qa = smem_addr(sQ + t * C::kTile), ka = smem_addr(sKV + (i % kSlots) * C::kTile);
+      const auto scores = [&](int t, int slot) {  // S_t = Q_t K^T; by the elected lane
+        const uint32_t qa = q_lo + t * (C::kTile / 16), ka = k_lo + slot * (C::kTile / 16);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          const uint32_t off = (k >> 2) * kBox + (k & 3) * 32;
-          mma_bf16(tmem + t * kKeys, smem_desc_k_sw128(qa + off), smem_desc_k_sw128(ka + off), kIdescS, k != 0);
+          const uint32_t off = ((k >> 2) * kBox + (k & 3) * 32) / 16;
+          mma_bf16(tmem + t * kKeys, qa + off, ka + off, kIdescS, k != 0);
         }
         mma_commit(&s_bar[t]);
       };
-      wait_full(0);
-      if (ok) {
-        for (int t = 0; t < 2; ++t)
-          if ((t ? count_b : count_a) > 0) scores(t, 0);
-        mma_commit(&empty_bar[0]);
+      const int slot0 = wait_item();
+      if (ok && elect_one()) {
+        if (count_a > 0) scores(0, slot0);
+        if (count_b > 0) scores(1, slot0);
+        mma_commit(&empty_bar[slot0]);
       }
+      __syncwarp();
       for (int j = 0; j < most && ok; ++j) {
-        const int iv = 2 * j + 1, ik = iv + 1;
-        wait_full(iv);
-        if (ok && j + 1 < most) wait_full(ik);
+        const int v_slot = wait_item();
+        const int k_slot = j + 1 < most ? wait_item() : 0;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int count = t ? count_b : count_a;
           if (!ok || j >= count) continue;
-          if (!mbar_wait_bounded(&p_bar[t], static_cast<uint32_t>(j) & 1u, abort_flag, limit_ns)) {
-            ok = false;
-            continue;
-          }
-          tc_fence_after();
-          const uint32_t va = smem_addr(sKV + (iv % kSlots) * C::kTile);
+          const uint32_t va = v_lo + v_slot * (C::kTile / 16);
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            mma_bf16_ta(tmem + kOCol + t * kKeys, tmem + t * kKeys + 8 * k, smem_desc_mn_sw128(va + 2048 * k, kBox),
-                        kIdescO, (j | k) != 0);
-          // the next scores overwrite the weights just read: the tensor core works in order
-          if (j + 1 < count)
-            scores(t, ik);
-          else
-            mma_commit(&o_bar[t]);
+          for (int half = 0; half < 2; ++half) {  // 64 keys as soon as their weights are there
+            if (ok)
+              ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&p_bar[2 * t + half], static_cast<uint32_t>(j) & 1u,
+                                                             abort_flag, limit_ns));
+            if (!ok) continue;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 4 * half; k < 4 * half + 4; ++k)
+                mma_bf16_ta(tmem + kOCol + t * 128, tmem + t * kKeys + 8 * k, va + 2048 / 16 * k, kIdescO, (j | k) != 0);
+              if (half == 1) {
+                // the next scores overwrite the weights just read: the tensor core works in order
+                if (j + 1 < count)
+                  scores(t, k_slot);
+                else
+                  mma_commit(&o_bar[t]);
+              }
+            }
+            __syncwarp();
+          }
         }
-        if (ok) {
-          mma_commit(&empty_bar[iv % kSlots]);
-          if (j + 1 < most) mma_commit(&empty_bar[ik % kSlots]);
+        if (ok && elect_one()) {
+          mma_commit(&empty_bar[v_slot]);
+          if (j + 1 < most) mma_commit(&empty_bar[k_slot]);
         }
+        __syncwarp();
       }
-      if (!ok) {
+      if (!ok && elect_one()) {
         record_error(a.status, W8A8_ERR_DEVICE_TIMEOUT);
         *abort_flag = 1;
         mma_commit(drain_bar);  // MMAs in flight finish before TMEM is freed
         mbar_wait_bounded(drain_bar, 0, nullptr, limit_ns / 16 + 1);
       }
+      __syncwarp();
     }
-  } else if (work) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if (work) {
     // -------------------------------------------------- softmax
     const int count = w ? count_b : count_a;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + static_cast<uint32_t>(w * kKeys);
-    const uint32_t t_o = t_s + kOCol;
+    const uint32_t t_o = tmem + lanes + kOCol + static_cast<uint32_t>(w * 128);
     const int pos = real ? seq.pos0() + my_tok0 + tok : -1;
     const int pos_min = seq.pos0() + my_tok0, pos_max = pos_min + my_toks - 1;
     const bool cap = a.softcap > 0.0f;
@@ -336,22 +391,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool plain = !cap && !a.slopes && a.scale >= 0.0f;  // a granule's largest score is its largest product
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
-    float4 kc4[2], vc4[2];
     const float *ks = x.ks + krow / kGran, *vs = x.vs + krow / kGran;
-    const auto fetch_scales = [&](int j) {
-      const int64_t at = static_cast<int64_t>(walk.tile(j)) * (kKeys / kGran);
+    for (int j = 0; j < count; ++j) {
+      const int key0 = walk.tile(j) * kKeys;
+      float kc[8], vc[8];  // scales of the tile's granules
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        kc4[e] = *reinterpret_cast<const float4 *>(ks + at + 4 * e);
-        vc4[e] = *reinterpret_cast<const float4 *>(vs + at + 4 * e);
+        const float4 k4 = *reinterpret_cast<const float4 *>(ks + key0 / kGran + 4 * e);
+        const float4 v4 = *reinterpret_cast<const float4 *>(vs + key0 / kGran + 4 * e);
+        kc[4 * e] = k4.x, kc[4 * e + 1] = k4.y, kc[4 * e + 2] = k4.z, kc[4 * e + 3] = k4.w;
+        vc[4 * e] = v4.x, vc[4 * e + 1] = v4.y, vc[4 * e + 2] = v4.z, vc[4 * e + 3] = v4.w;
       }
-    };
-    if (count > 0) fetch_scales(0);
-    for (int j = 0; j < count; ++j) {
-      float kc[8] = {kc4[0].x, kc4[0].y, kc4[0].z, kc4[0].w, kc4[1].x, kc4[1].y, kc4[1].z, kc4[1].w};
-      const float vc[8] = {vc4[0].x, vc4[0].y, vc4[0].z, vc4[0].w, vc4[1].x, vc4[1].y, vc4[1].z, vc4[1].w};
-      if (j + 1 < count) fetch_scales(j + 1);
-      const int key0 = walk.tile(j) * kKeys;
       bool whole = key0 + kKeys - 1 <= pos_min && (a.window == 0 || key0 > pos_max - a.window);
 #pragma unroll
       for (int g = 0; g < 8; ++g) whole = whole && kc[g] != -1.0f;
@@ -360,47 +410,100 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
+      // the row's scores, all of them in flight at once
+      uint32_t s0[32], s1[32], s2[32], s3[32];
+      tmem_ld_32x32b_x32(t_s, s0);
+      tmem_ld_32x32b_x32(t_s + 32, s1);
+      tmem_ld_32x32b_x32(t_s + 64, s2);
+      tmem_ld_32x32b_x32(t_s + 96, s3);
+      tmem_ld_wait();
       float top = -INFINITY;
       if (whole && plain) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s[32];
-          tmem_ld_32x32b_x32(t_s + 32 * c, s);
-          tmem_ld_wait();
+        const auto largest = [&](const uint32_t(&s)[32], int c) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            float v = __uint_as_float(s[16 * g]);
+            float v = __uint_as_float(s[16 * g]), u = __uint_as_float(s[16 * g + 1]);
 #pragma unroll
-            for (int e = 1; e < 16; ++e) v = fmaxf(v, __uint_as_float(s[16 * g + e]));
-            top = fmaxf(top, v * (kc[2 * c + g] * mul));
+            for (int e = 2; e < 16; e += 4) {
+              v = max3(v, __uint_as_float(s[16 * g + e]), __uint_as_float(s[16 * g + e + 1]));
+              if (e + 2 < 16) u = max3(u, __uint_as_float(s[16 * g + e + 2]), __uint_as_float(s[16 * g + e + 3]));
+            }
+            kc[2 * c + g] *= mul;
+            top = fmaxf(top, fmaxf(v, u) * kc[2 * c + g]);
           }
-        }
+        };
+        largest(s0, 0);
+        largest(s1, 1);
+        largest(s2, 2);
+        largest(s3, 3);
+      } else {  // element by element
+        const float far = slope * static_cast<float>(key0 - pos);
+        // keys key0 + e of this row: e <= hi and e >= lo, or e < pre
+        const int hi = pos < 0 ? -1 : min(pos, seq.n - 1) - key0;
+        const int lo = a.window > 0 ? pos - a.window + 1 - key0 : -key0;
+        const int pre = pos < 0 ? 0 : min(prefix, seq.n) - key0;
+        // CAP: tanh cap; BIAS: distance bias; MASK: some row of the tile does
+        // not see some key (CAP decides about the other two as it goes)
+        const auto finish = [&](auto cap_c, auto bias_c, auto mask_c, uint32_t(&s)[32], int c) {
+          constexpr bool CAP = decltype(cap_c)::value, BIAS = decltype(bias_c)::value, MASK = decltype(mask_c)::value;
 #pragma unroll
-        for (int g = 0; g < 8; ++g) kc[g] *= mul;
-      } else {  // element by element; the finished scores go back to TMEM
+          for (int g = 0; g < 2; ++g) {
+            const float k1 = kc[2 * c + g], f = k1 * mul;
+            const int e0 = 32 * c + 16 * g;
+            float y[16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s[32];
-          tmem_ld_32x32b_x32(t_s + 32 * c, s);
-          tmem_ld_wait();
+            for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(s[16 * g + i]);
+            if constexpr (CAP) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float k1 = kc[2 * c + (e >> 4)];
-            float v = __uint_as_float(s[e]) * (k1 * mul);
-            if (cap) v = cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(v * (2.0f * kLog2e)));
-            const int key = key0 + 32 * c + e;
-            v += slope * static_cast<float>(key - pos);
-            const bool seen = k1 != -1.0f && key < seq.n && pos >= 0 &&
-                              ((key <= pos && (a.window == 0 || pos - key < a.window)) || key < prefix);
-            v = seen ? v : -INFINITY;
-            top = fmaxf(top, v);
-            s[e] = __float_as_uint(v);
+              for (int i = 0; i < 16; ++i)
+                y[i] = cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(y[i] * (f * (2.0f * kLog2e))));
+            }
+            if constexpr (BIAS) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                float b0 = fmaf(slope, static_cast<float>(e0 + i), far), b1 = fmaf(slope, static_cast<float>(e0 + i + 1), far);
+                axpy2(b0, b1, y[i], y[i + 1], CAP ? 1.0f : f);
+                y[i] = b0, y[i + 1] = b1;
+              }
+            } else if constexpr (!CAP) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) mul_f32x2(y[i], y[i + 1], f, y[i], y[i + 1]);
+            }
+            if constexpr (MASK) {
+              // bits of the granule's keys that this row sees
+              uint32_t seen = (bits_below(hi + 1 - e0) & ~bits_below(lo - e0)) | bits_below(pre - e0);
+              if (k1 == -1.0f) seen = 0;
+              // a page of which this row sees nothing may hold anything: its weights are 0 times 0
+              if (seen == 0) vc[2 * c + g] = 0.0f;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) y[i] = (seen >> i) & 1u ? y[i] : -INFINITY;
+            }
+            float v = y[0], u = y[1];
+#pragma unroll
+            for (int i = 2; i < 16; i += 4) {
+              v = max3(v, y[i], y[i + 1]);
+              if (i + 2 < 16) u = max3(u, y[i + 2], y[i + 3]);
+            }
+            top = max3(top, v, u);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[16 * g + i] = __float_as_uint(y[i]);
+            kc[2 * c + g] = 1.0f;
           }
-          tmem_st_32x32b_x32(t_s + 32 * c, s);
-        }
-        tmem_st_wait();
-#pragma unroll
-        for (int g = 0; g < 8; ++g) kc[g] = 1.0f;
+        };
+        const auto finish_row = [&](auto cap_c, auto bias_c, auto mask_c) {
+          finish(cap_c, bias_c, mask_c, s0, 0);
+          finish(cap_c, bias_c, mask_c, s1, 1);
+          finish(cap_c, bias_c, mask_c, s2, 2);
+          finish(cap_c, bias_c, mask_c, s3, 3);
+        };
+        if (cap)
+          finish_row(Yes(), Yes(), Yes());
+        else if (a.slopes && whole)
+          finish_row(No(), Yes(), No());
+        else if (a.slopes)
+          finish_row(No(), Yes(), Yes());
+        else
+          finish_row(No(), No(), Yes());
       }
       const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
       if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -408,51 +511,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (grow) m = top;
         l *= fr;
         if (j > 0) {  // O_w(j - 1) is complete, O_w(j) waits for this warp
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(t_o + 32 * c, o);
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(t_o + 16 * c, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fr);
-            tmem_st_32x32b_x32(t_o + 32 * c, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fr);
+            tmem_st_32x32b_x16(t_o + 16 * c, o);
           }
         }
       }
       const float ref = m == -INFINITY ? 0.0f : -m;
-      float l0 = 0.0f, l1 = 0.0f;
+      float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
+      // 32 weights, packed by two; stage by stage over a granule, so that the
+      // steps of 16 independent elements overlap
+      uint32_t p[32];
+      const auto weights = [&](const uint32_t(&s)[32], int c) {
 #pragma unroll
-      for (int c2 = 0; c2 < 2; ++c2) {
-        uint32_t p[32];
+        for (int h2 = 0; h2 < 2; ++h2) {
+          const int g = 2 * c + h2;
+          float y[16];
 #pragma unroll
-        for (int c1 = 0; c1 < 2; ++c1) {
-          const int c = 2 * c2 + c1;
-          uint32_t s[32];
-          tmem_ld_32x32b_x32(t_s + 32 * c, s);
-          tmem_ld_wait();
+          for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(s[16 * h2 + e]);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const int g = 2 * c + (e >> 4);
-            float s0 = __uint_as_float(s[e]), s1 = __uint_as_float(s[e + 1]);
-            fma2(s0, s1, kc[g], ref);
-            float p0 = ex2(s0), p1 = ex2(s1);
-            add2(l0, l1, p0, p1);
-            if (whole) {
-              mul_f32x2(p0, p1, vc[g], p0, p1);
-            } else {  // (not 0 times the scale of a page that no row sees, which may be anything)
-              p0 = p0 > 0.0f ? p0 * vc[g] : 0.0f;
-              p1 = p1 > 0.0f ? p1 * vc[g] : 0.0f;
-            }
-            p[16 * c1 + (e >> 1)] = pack_bf16x2(p0, p1);
+          for (int e = 0; e < 16; e += 2) fma2(y[e], y[e + 1], kc[g], ref);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = ex2(y[e]);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            add2(l0, l1, y[e], y[e + 1]);
+            add2(l2, l3, y[e + 2], y[e + 3]);
           }
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) mul_f32x2(y[e], y[e + 1], vc[g], y[e], y[e + 1]);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) p[16 * (c & 1) + 8 * h2 + (e >> 1)] = pack_bf16x2(y[e], y[e + 1]);
         }
-        tmem_st_32x32b_x32(t_s + 32 * c2, p);  // columns whose scores have been read
-      }
-      l += l0 + l1;
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_bar[w]);
+      };
+      const auto hand_over = [&](int half) {  // the weights of 64 keys, over scores that have been read
+        tmem_st_32x32b_x32(t_s + 32 * half, p);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_bar[2 * w + half]);
+      };
+      weights(s0, 0);
+      weights(s1, 1);
+      hand_over(0);
+      weights(s2, 2);
+      weights(s3, 3);
+      hand_over(1);
+      l += (l0 + l1) + (l2 + l3);
     }
     if (ok && count > 0)
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&o_bar[w], 0, abort_flag, limit_ns));
@@ -464,42 +574,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       tc_fence_after();
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      const int64_t elem = (static_cast<int64_t>(seq.row0 + my_tok0 + tok) * a.q_heads + hq) * D;
+      // rows through the query tile's memory (its last product is complete), then out by neighbouring lanes
+      uint8_t *const stage = sQ + w * C::kTile;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t o[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0;
+        for (int e = 0; e < 16; ++e) o[e] = 0;
         if (count > 0) {
-          tmem_ld_32x32b_x32(t_o + 32 * c, o);
+          tmem_ld_32x32b_x16(t_o + 16 * c, o);
           tmem_ld_wait();
         }
-        if (real) {
-          uint32_t y[16];
+        uint32_t y[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            y[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          if (!a.r_out) {
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + elem + 32 * c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-          } else {
-            const float r = __ldg(a.r_out);
-            const int z = __ldg(a.z_out);
-            uint2 *dst = reinterpret_cast<uint2 *>(static_cast<int8_t *>(a.out) + elem + 32 * c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = quant8_asym_sat(make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]), r, z);
-          }
-        }
+        for (int e = 0; e < 8; ++e)
+          y[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+        uint8_t *const at = stage + row * 128 + (c >> 2) * kBox;
+        const int c0 = (2 * c) & 7;
+        *reinterpret_cast<uint4 *>(at + ((c0 ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4 *>(at + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+      }
+      __syncwarp();
+      const float r_out = a.r_out ? __ldg(a.r_out) : 0.0f;
+      const int z_out = a.r_out ? __ldg(a.z_out) : 0;
+#pragma unroll 4
+      for (int i = lane; i < 32 * (D / 8); i += 32) {
+        const int r = (warp & 3) * 32 + i / (D / 8), c = i % (D / 8);
+        const int r_tok = r / a.group;
+        if (r_tok >= my_toks) continue;
+        const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 128 + (c >> 3) * kBox + (((c & 7) ^ (r & 7)) << 4));
+        const int64_t elem = (static_cast<int64_t>(seq.row0 + my_tok0 + r_tok) * a.q_heads + h * a.group +
+                              (r - r_tok * a.group)) * D + 8 * c;
+        if (!a.r_out)
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + elem) = v;
+        else
+          *reinterpret_cast<uint2 *>(static_cast<int8_t *>(a.out) + elem) = quant8_asym_sat(v, r_out, z_out);
       }
     }
+    }
   }
-
   tc_fence_before();
   __syncwarp();  // lanes of the producer and MMA warps reconverge before the CTA barrier
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kSoftmaxWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }

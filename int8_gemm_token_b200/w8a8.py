@@ -515,8 +515,10 @@ class PagedKVCache:
             raise ValueError(f"k_codes: head dim must be 64, 96 or 128, got {shape[3]}")
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = shape
-        self.device = k_codes.device
+        self.device, self._dev = k_codes.device, k_codes.get_device()
         self._tensors = (k_codes, v_codes, k_scale, v_scale)
+        if any(t.device != self.device for t in self._tensors):
+            raise ValueError(f"expected tensors on one device, got {sorted({str(t.device) for t in self._tensors})}")
         self._c = _CacheStruct(*(t.data_ptr() for t in self._tensors), *shape)
         self._ref = ctypes.byref(self._c)
 
@@ -543,8 +545,9 @@ class KVBatch:
         _vec(kv_len, torch.int32, batch, "kv_len")
         self.page_table, self.seq_start, self.kv_len = page_table, seq_start, kv_len
         self.max_q_len, self.max_kv_len = int(max_q_len), max_kv_len
-        self._tensors = (page_table, seq_start, kv_len)
-        self._max_pages = max_pages
+        if seq_start.device != page_table.device or kv_len.device != page_table.device:
+            raise ValueError("expected page_table, seq_start and kv_len on one device")
+        self.size, self._max_pages = batch, max_pages
         self._c = _BatchStruct(page_table.data_ptr(), max(ld, max_pages), seq_start.data_ptr(), kv_len.data_ptr(),
                                batch, max_pages, self.max_q_len, 0)
         self._ref = ctypes.byref(self._c)
@@ -556,30 +559,63 @@ class KVBatch:
         return self._ref
 
 
-def _heads3(t, heads, d, what: str, tokens=None):
-    """A bf16 tensor [tokens, heads, d] whose last axis is contiguous; returns
-    its strides between tokens and heads in elements."""
+# These calls run once or more for every layer of a Decode step of a few
+# microseconds, so their marshalling is kept short: each tensor is looked at
+# once (dtype, shape, strides, device index) and what does not change between
+# steps was checked when the PagedKVCache and KVBatch were made.
+
+def _bad(what: str, expected: str, t):
     if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what}: expected a tensor, got {type(t).__name__}")
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads) \
-            or (tokens is not None and t.shape[0] != tokens) or t.stride(2) != 1:
-        raise ValueError(f"{what}: expected bfloat16 [{'tokens' if tokens is None else tokens}, "
-                         f"{'heads' if heads is None else heads}, {d}] with a contiguous last axis, "
-                         f"got {t.dtype} {tuple(t.shape)} strides {tuple(t.stride())}")
-    st, sh = t.stride(0), t.stride(1)
-    # the stride of an axis of one (or no) element is never used; torch may report any value for it
-    return (st if t.shape[0] > 1 else 0), (sh if t.shape[1] > 1 else 0)
+        return TypeError(f"{what}: expected a tensor, got {type(t).__name__}")
+    return ValueError(f"{what}: expected {expected}, got {t.dtype} {tuple(t.shape)} strides {tuple(t.stride())}")
 
 
-def _kv_call(fn, dev, stream, *args):
-    """Call entry point `fn` with `dev` current, on the given stream or dev's current one."""
-    f = getattr(lib(), fn)
-    if dev.index is not None and dev.index != torch.cuda.current_device():
+def _heads3(t, heads, d, what: str, tokens=None):
+    """A bf16 tensor [tokens, heads, d] whose last axis is contiguous: its
+    shape and its strides between tokens and heads in elements."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16:
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 3 and shape[2] == d and stride[2] == 1 and (heads is None or shape[1] == heads) \
+                and (tokens is None or shape[0] == tokens):
+            # the stride of an axis of one (or no) element is never used; torch may report any value for it
+            return shape[0], shape[1], (stride[0] if shape[0] > 1 else 0), (stride[1] if shape[1] > 1 else 0)
+    raise _bad(what, f"bfloat16 [{'tokens' if tokens is None else tokens}, {'heads' if heads is None else heads}, {d}] "
+                     "with a contiguous last axis", t)
+
+
+def _dense(t, dtype, shape, what: str):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise _bad(what, f"a contiguous {dtype} tensor of shape {tuple(shape)}", t)
+
+
+def _same_gpu(dev: int, *ts):
+    """Every tensor on the GPU of that index (checked after the shapes, as in _on_one_gpu)."""
+    for t in ts:
+        if t is not None and t.get_device() != dev or dev < 0:
+            raise ValueError(f"expected CUDA tensors on one device, got {sorted({str(t.device) for t in ts if t is not None})}")
+
+
+_entry = {}
+
+
+def _kv_fn(name):
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(lib(), name)
+    return f
+
+
+def _kv_call(fn, dev: int, stream, *args):
+    """Call entry point `fn` with GPU `dev` current, on the given stream or the GPU's current one."""
+    f = _kv_fn(fn)
+    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            status = f(*args, _stream(stream))
+            status = f(*args, raw)
     else:
-        status = f(*args, _stream(stream))
-    _check(fn, status)
+        status = f(*args, raw)
+    if status:
+        _check(fn, status)
 
 
 def w8a8_kv_append(k, v, cache: PagedKVCache, batch: KVBatch, cos=None, sin=None, q=None, q_out=None,
@@ -587,31 +623,36 @@ def w8a8_kv_append(k, v, cache: PagedKVCache, batch: KVBatch, cos=None, sin=None
     """Rotate (cos, sin fp32 [positions, rot_dim / 2]), quantize and store the
     new tokens' keys and values; with q, rotate the queries into q_out (bf16
     [tokens, q_heads, head_dim], allocated when None; returned)."""
-    d = cache.head_dim
-    kst, ksh = _heads3(k, cache.kv_heads, d, "k")
-    tokens = k.shape[0]
-    vst, vsh = _heads3(v, cache.kv_heads, d, "v", tokens)
-    rope_len = rot = 0
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin: give both or neither")
+    d, dev = cache.head_dim, cache._dev
+    tokens, _, kst, ksh = _heads3(k, cache.kv_heads, d, "k")
+    _, _, vst, vsh = _heads3(v, cache.kv_heads, d, "v", tokens)
+    rope_len = half = 0
+    cp = sp = qp = op = None
     if cos is not None:
-        if cos.dim() != 2:
-            raise ValueError(f"cos: expected [positions, rot_dim / 2], got {tuple(cos.shape)}")
-        _expect(cos, torch.float32, tuple(cos.shape), "cos")
-        _expect(sin, torch.float32, tuple(cos.shape), "sin")
-        rope_len, rot = cos.shape[0], 2 * cos.shape[1]
+        if sin is None:
+            raise ValueError("cos and sin: give both or neither")
+        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+            raise _bad("cos", "float32 [positions, rot_dim / 2]", cos)
+        shape = cos.shape
+        _dense(cos, torch.float32, shape, "cos")
+        _dense(sin, torch.float32, shape, "sin")
+        rope_len, half = shape
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    elif sin is not None:
+        raise ValueError("cos and sin: give both or neither")
     qst = qsh = hq = 0
     if q is not None:
-        qst, qsh = _heads3(q, None, d, "q", tokens)
-        hq = q.shape[1]
+        _, hq, qst, qsh = _heads3(q, None, d, "q", tokens)
         if q_out is None:
             q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
-        _expect(q_out, torch.bfloat16, (tokens, hq, d), "q_out")
+        else:
+            _dense(q_out, torch.bfloat16, (tokens, hq, d), "q_out")
+        qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out: given without q")
-    _on_one_gpu(k, v, cos, sin, q, q_out, *cache._tensors, *batch._tensors)
-    _kv_call("w8a8_kv_append", cache.device, stream, cache._ref, batch._for(cache), tokens, _ptr(k), kst, ksh, _ptr(v),
-             vst, vsh, _ptr(cos), _ptr(sin), rope_len, rot, int(bool(interleaved)), _ptr(q), qst, qsh, hq, _ptr(q_out))
+    _same_gpu(dev, k, v, cos, sin, q, q_out, batch.page_table)
+    _kv_call("w8a8_kv_append", dev, stream, cache._ref, batch._for(cache), tokens, k.data_ptr(), kst, ksh, v.data_ptr(),
+             vst, vsh, cp, sp, rope_len, 2 * half, 1 if interleaved else 0, qp, qst, qsh, hq, op)
     return q_out
 
 
@@ -623,56 +664,64 @@ def w8a8_kv_gather(cache: PagedKVCache, page_table, first_pos, row_start, rows: 
     given) -> (k_out, v_out)."""
     ld = _rows(page_table, torch.int32, "page_table")
     batch, max_pages = page_table.shape
-    _vec(first_pos, torch.int32, batch, "first_pos")
-    _vec(row_start, torch.int32, batch + 1, "row_start")
+    _dense(first_pos, torch.int32, (batch,), "first_pos")
+    _dense(row_start, torch.int32, (batch + 1,), "row_start")
     given = k_out if k_out is not None else v_out
     if given is None:
         if rows is None:
             raise ValueError("rows: required where no output is given")
         shape = (int(rows), cache.kv_heads, cache.head_dim)
-        k_out = _out(None, out_dtype, shape, cache.device, (torch.bfloat16, torch.float32), "k_out")
+        given = k_out = _out(None, out_dtype, shape, cache.device, (torch.bfloat16, torch.float32), "k_out")
         v_out = torch.empty_like(k_out)
-        given = k_out
-    shape = (given.shape[0] if rows is None else int(rows), cache.kv_heads, cache.head_dim)
-    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None:
-            _out(t, None, shape, None, (torch.bfloat16, torch.float32), what)
-            if t.dtype != given.dtype:
-                raise ValueError("v_out: expected the type of k_out")
-    _on_one_gpu(page_table, first_pos, row_start, k_out, v_out, *cache._tensors)
-    _kv_call("w8a8_kv_gather", cache.device, stream, cache._ref, _ptr(page_table), max(ld, max_pages), batch, max_pages,
-             _ptr(first_pos), _ptr(row_start), shape[0], _ptr(k_out), _ptr(v_out), _dt(given.dtype))
+    else:
+        what = "k_out" if k_out is not None else "v_out"
+        if not isinstance(given, torch.Tensor) or given.dtype not in (torch.bfloat16, torch.float32) or given.dim() != 3:
+            raise _bad(what, "bfloat16 or float32 [rows, kv_heads, head_dim]", given)
+        shape = (given.shape[0] if rows is None else int(rows), cache.kv_heads, cache.head_dim)
+        _dense(given, given.dtype, shape, what)
+        if k_out is not None and v_out is not None:
+            _dense(v_out, given.dtype, shape, "v_out")
+    _same_gpu(cache._dev, page_table, first_pos, row_start, k_out, v_out)
+    _kv_call("w8a8_kv_gather", cache._dev, stream, cache._ref, page_table.data_ptr(), ld if ld > max_pages else max_pages,
+             batch, max_pages, first_pos.data_ptr(), row_start.data_ptr(), shape[0],
+             None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
+             BF16 if given.dtype is torch.bfloat16 else FP32)
     return k_out, v_out
 
 
 def w8a8_kv_attention_workspace_size(cache: PagedKVCache, batch: KVBatch, tokens: int, q_heads: int) -> int:
-    return int(lib().w8a8_kv_attention_workspace_size(cache._ref, batch._for(cache), tokens, q_heads))
+    """Bytes of workspace the attention calls need, on the cache's GPU."""
+    f = _kv_fn("w8a8_kv_attention_workspace_size")
+    if cache._dev >= 0 and cache._dev != torch.cuda.current_device():
+        with torch.cuda.device(cache._dev):
+            return f(cache._ref, batch._for(cache), tokens, q_heads)
+    return f(cache._ref, batch._for(cache), tokens, q_heads)
 
 
 def _attention(fn, q, cache, batch, scale, softcap, window, slopes, prefix_len, out, out_dtype, extra, workspace, stream):
-    d = cache.head_dim
-    qst, qsh = _heads3(q, None, d, "q")
-    tokens, hq, _ = q.shape
-    _vec(slopes, torch.float32, hq, "slopes", optional=True)
-    _vec(prefix_len, torch.int32, batch.kv_len.shape[0], "prefix_len", optional=True)
+    d, dev = cache.head_dim, cache._dev
+    tokens, hq, qst, qsh = _heads3(q, None, d, "q")
+    sp = pp = None
+    if slopes is not None:
+        _dense(slopes, torch.float32, (hq,), "slopes")
+        sp = slopes.data_ptr()
+    if prefix_len is not None:
+        _dense(prefix_len, torch.int32, (batch.size,), "prefix_len")
+        pp = prefix_len.data_ptr()
     if out is None:
         out = torch.empty((tokens, hq, d), dtype=out_dtype, device=q.device)
-    _expect(out, out_dtype, (tokens, hq, d), "out")
-    _on_one_gpu(q, slopes, prefix_len, out, workspace, *extra, *cache._tensors, *batch._tensors)
-    bref = batch._for(cache)
+    else:
+        _dense(out, out_dtype, (tokens, hq, d), "out")
+    _same_gpu(dev, q, out, slopes, prefix_len, workspace, batch.page_table, *extra)
     if workspace is None:
-        if cache.device.index is not None and cache.device.index != torch.cuda.current_device():
-            with torch.cuda.device(cache.device):
-                need = int(lib().w8a8_kv_attention_workspace_size(cache._ref, bref, tokens, hq))
-        else:
-            need = int(lib().w8a8_kv_attention_workspace_size(cache._ref, bref, tokens, hq))
-        workspace, nbytes = _workspace(need, q.device, None)
+        nbytes = w8a8_kv_attention_workspace_size(cache, batch, tokens, hq)
+        if nbytes:
+            workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
     else:
         workspace, nbytes = _workspace(0, q.device, workspace)
-    sc = _ScoresStruct(d ** -0.5 if scale is None else float(scale), float(softcap), _ptr(slopes), int(window),
-                       _ptr(prefix_len))
-    _kv_call(fn, cache.device, stream, cache._ref, bref, tokens, _ptr(q), qst, qsh, hq, ctypes.byref(sc),
-             *(_ptr(t) for t in extra), _ptr(out), _ptr(workspace), nbytes)
+    sc = _ScoresStruct(d ** -0.5 if scale is None else scale, softcap, sp, window, pp)
+    _kv_call(fn, dev, stream, cache._ref, batch._for(cache), tokens, q.data_ptr(), qst, qsh, hq, ctypes.byref(sc),
+             *[t.data_ptr() for t in extra], out.data_ptr(), None if workspace is None else workspace.data_ptr(), nbytes)
     return out
 
 
