@@ -132,7 +132,7 @@ w8a8_status run_attention(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch
   const size_t need = workspace_bytes_of(a, sms);
   if (need > 0 && (!workspace || workspace_bytes < need)) return W8A8_ERR_WORKSPACE;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return from_cuda(few_rows(a) ? launch_kv_decode(a, workspace, sms, st) : launch_kv_prefill(a, workspace, st));
+  return from_cuda(few_rows(a) ? launch_kv_decode(a, workspace, sms, st) : launch_kv_prefill(a, workspace, sms, st));
 }
 
 }  // namespace

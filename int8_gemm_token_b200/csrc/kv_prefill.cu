@@ -9,21 +9,27 @@
 //   [sequence][kv head][key][dim] matrices, 128-key tiles zero-padded, with
 //   the scales of each granule of 16 keys beside them. Every key tile is used
 //   by many query tiles; expanded once, it comes back through TMA in the
-//   layout the MMAs read and no query tile converts anything.
-//   kv_prefill_kernel: a block per 256 query rows of one kv head, in two
+//   layout the MMAs read and no query tile converts anything. One of its
+//   blocks lists the query blocks, those with the most key tiles first.
+//   kv_prefill_kernel: persistent, one block per SM, which takes (query
+//   block, kv head) items from that list. An item is 256 query rows in two
 //   tiles of 128 = floor(128 / group) tokens x group heads, so that grouped
 //   heads share their key tiles. Roles:
 //     warps 0-3, 4-7  softmax of tile A and of tile B, one thread per row:
 //                 S from TMEM (tcgen05.ld), maximum, 2^(s - m), row sum, and
 //                 the weights times v's scale back into TMEM as the bf16 A
 //                 operand of the second product (over S, which is dead by
-//                 then); at the end O / l to global memory;
-//     warp 8      TMA producer: 128-byte-swizzled 128 x 64 boxes of K and V
-//                 into a ring of key tiles;
+//                 then); at the end O / l to global memory, through shared
+//                 memory so that neighbouring lanes store neighbouring bytes;
+//     warp 8      takes items and loads 128-byte-swizzled 128 x 64 boxes of
+//                 K and V (TMA) into a ring of key tiles;
 //     warp 9      MMA issuer: S = Q K^T (both K-major in shared memory) and
 //                 O += P V (P in TMEM, V as an MN-major operand, so V needs
 //                 no transpose). While one tile's softmax runs, the other
-//                 tile's products do.
+//                 tile's products do; the next item's first scores are
+//                 computed while this one's output is written;
+//     warps 10, 11  load the next item's query rows (cp.async) as soon as the
+//                 last scores of this one are done.
 //   The page scales never touch the operands: k's multiplies the scores (a
 //   granule's maximum is scaled once, an element's factor is that of the
 //   fused multiply-add before 2^x), v's multiplies the weights.
@@ -45,7 +51,9 @@ constexpr int kRows = 128;             // query rows of a tile = TMEM lanes
 constexpr int kBox = kKeys * 128;      // bytes of a 64-dim box of 128 rows
 constexpr int kSlots = 4;              // key tiles (K or V) in flight
 constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // softmax, producer, MMA, two idle
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // softmax, key tiles, MMA, two for query rows
+constexpr int kStageRow = 128;         // bytes of a row in a softmax warp's output staging (64 dims)
+constexpr int kStage = 32 * kStageRow;
 // Registers a thread: 168 at launch (65536 / 384); a softmax thread holds a
 // whole row of 128 scores and wants more, the others few.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
@@ -59,25 +67,106 @@ struct PCfg {
   static constexpr int kAtoms = D > 64 ? 2 : 1;       // 64-dim boxes of a row
   static constexpr int kPitch = 64 * kAtoms;          // elements of an expanded row
   static constexpr int kTile = kAtoms * kBox;         // bytes of a K, V or Q tile
-  static constexpr size_t kSmem = static_cast<size_t>(2 + kSlots) * kTile + 1024 + 256;
+  static constexpr size_t kSmem = static_cast<size_t>(2 + kSlots) * kTile + kSoftmaxWarps * kStage + 1024 + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
 
 int64_t expanded_len(int32_t max_kv) { return (static_cast<int64_t>(max_kv) + kKeys - 1) / kKeys * kKeys; }
 
 // ------------------------------------------------------------------ expansion
-// Block: 64 keys of one (kv head, sequence). Rows from the sequence's end to
+// Block (x > 0): 64 keys of one (kv head, sequence). Rows from the sequence's end to
 // the end of its last 128-key tile are zeros (they meet weights of 0, and
 // must not be NaN). A granule's scales: of its page; 0 past the end; -1 for a
 // page that does not exist.
 constexpr int kExpandKeys = 64;
 constexpr int kExpandThreads = 256;
 
+// A query block: its first packed row, the position of that row's token, its
+// tokens (of 2 floor(128 / group) at most), and its sequence.
+struct __align__(16) QueryBlock {
+  int32_t row, pos, toks, b;
+  int32_t n, prefix, pad0, pad1;
+};
+
 struct Expanded {
   uint16_t *k, *v;      // [sequence][head][len][pitch]
   float *ks, *vs;       // [sequence][head][len / 16]
   int64_t len;
+  int32_t *counters;    // [0] query blocks listed, [1] items taken
+  QueryBlock *blocks;   // those with the most key tiles first
+  int32_t slots;        // room in the list
 };
+
+// The list of query blocks, by one block of kExpandThreads threads: a counting
+// sort by the number of key tiles, descending. Slot f(b) = seq_start[b] / T + b
+// leaves sequence b room for its ceil(q / T) blocks of T tokens. The order of
+// blocks with equally many tiles is left open; it decides only where and when
+// a block runs.
+constexpr int kBins = 2048;
+
+__device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
+  __shared__ int32_t s_bin[kBins], s_sum[kExpandThreads];
+  const int T = 2 * (kRows / a.group), tid = threadIdx.x;
+  int shift = 0;
+  while ((x.len / kKeys) >> shift >= kBins) ++shift;
+  for (int i = tid; i < kBins; i += kExpandThreads) s_bin[i] = 0;
+  __syncthreads();
+  const auto block_of = [&](int32_t slot, QueryBlock &q, int &bin) {
+    int lo = 0, hi = a.s.batch;  // the last sequence whose slots begin at or before this one
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(a.s.seq_start + mid) / T + mid <= slot)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    const int b = lo - 1;
+    if (b < 0) return false;
+    const KvSeq seq = load_seq(a.s, b, a.s.max_kv, a.status);
+    const int64_t tok = static_cast<int64_t>(slot - (__ldg(a.s.seq_start + b) / T + b)) * T;
+    if (tok < 0 || tok >= seq.q) return false;
+    q.b = b;
+    q.row = seq.row0 + static_cast<int>(tok);
+    q.pos = seq.pos0() + static_cast<int>(tok);
+    q.toks = min(T, seq.q - static_cast<int>(tok));
+    q.n = seq.n;
+    q.prefix = a.prefix ? __ldg(a.prefix + b) : 0;
+    q.pad0 = q.pad1 = 0;
+    const int tiles = tile_walk(kKeys, q.prefix, q.n, max(q.pos, 0), q.pos + q.toks, a.window).count;
+    bin = kBins - 1 - min(tiles >> shift, kBins - 1);
+    return true;
+  };
+  QueryBlock q;
+  int bin = 0;
+  for (int slot = tid; slot < x.slots; slot += kExpandThreads)
+    if (block_of(slot, q, bin)) atomicAdd(&s_bin[bin], 1);
+  __syncthreads();
+  // exclusive scan of the bins, kBins / kExpandThreads to a thread
+  constexpr int PER = kBins / kExpandThreads;
+  int sum = 0;
+  for (int i = 0; i < PER; ++i) sum += s_bin[tid * PER + i];
+  s_sum[tid] = sum;
+  __syncthreads();
+  for (int o = 1; o < kExpandThreads; o <<= 1) {
+    const int v = tid >= o ? s_sum[tid - o] : 0;
+    __syncthreads();
+    s_sum[tid] += v;
+    __syncthreads();
+  }
+  int at = s_sum[tid] - sum;
+  for (int i = 0; i < PER; ++i) {
+    const int c = s_bin[tid * PER + i];
+    s_bin[tid * PER + i] = at;
+    at += c;
+  }
+  if (tid == kExpandThreads - 1) {
+    x.counters[0] = at;
+    x.counters[1] = 0;
+  }
+  __syncthreads();
+  for (int slot = tid; slot < x.slots; slot += kExpandThreads)
+    if (block_of(slot, q, bin)) x.blocks[atomicAdd(&s_bin[bin], 1)] = q;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kExpandThreads) kv_expand_kernel(const __grid_constant__ KvAttnArgs a,
@@ -86,7 +175,11 @@ __global__ void __launch_bounds__(kExpandThreads) kv_expand_kernel(const __grid_
   __shared__ int32_t s_page[kExpandKeys / kGran];
   pdl_launch_dependents();
   pdl_wait_prerequisite();
-  const int b = blockIdx.z, h = blockIdx.y, key0 = blockIdx.x * kExpandKeys;
+  if (blockIdx.x == 0) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) list_query_blocks(a, x);
+    return;
+  }
+  const int b = blockIdx.z, h = blockIdx.y, key0 = (blockIdx.x - 1) * kExpandKeys;
   const KvSeq seq = load_seq(a.s, b, a.s.max_kv, a.status);
   if (seq.q == 0 || key0 >= (seq.n + kKeys - 1) / kKeys * kKeys) return;
   const int32_t prefix = a.prefix ? __ldg(a.prefix + b) : 0;
@@ -163,25 +256,41 @@ __device__ __forceinline__ void add2(float &x0, float &x1, float y0, float y1) {
       : "f"(y0), "f"(y1));
 }
 
+// An item as its block's warps see it.
+struct Item {
+  QueryBlock q;
+  int32_t h, pad[3];
+};
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_prefill_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                      const __grid_constant__ KvAttnArgs a, const __grid_constant__ Expanded x, int64_t slots_total,
-                      uint64_t limit_ns) {
+                      const __grid_constant__ KvAttnArgs a, const __grid_constant__ Expanded x, uint64_t limit_ns) {
   using C = PCfg<D>;
   constexpr int KS = D / 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sQ = base;                    // two tiles
-  uint8_t *sKV = base + 2 * C::kTile;   // ring of key tiles
-  uint64_t *full_bar = reinterpret_cast<uint64_t *>(sKV + kSlots * C::kTile);
+  uint8_t *sQ = base;                                 // two tiles
+  uint8_t *sKV = base + 2 * C::kTile;                 // ring of key tiles
+  uint8_t *sStage = sKV + kSlots * C::kTile;          // [softmax warp] output staging
+  Item *s_item = reinterpret_cast<Item *>(sStage + kSoftmaxWarps * kStage);  // [2]
+  uint64_t *full_bar = reinterpret_cast<uint64_t *>(s_item + 2);
   uint64_t *empty_bar = full_bar + kSlots;
   uint64_t *s_bar = empty_bar + kSlots;  // [tile] scores are in TMEM
   uint64_t *p_bar = s_bar + 2;           // [tile][half of the keys] weights are (one arrival per softmax warp)
   uint64_t *o_bar = p_bar + 4;           // [tile] the output is final
-  uint64_t *drain_bar = o_bar + 2;
+  uint64_t *qfull_bar = o_bar + 2;       // [tile] query rows are in shared memory
+  uint64_t *qempty_bar = qfull_bar + 2;  // [tile] their last product is complete
+  uint64_t *ifull_bar = qempty_bar + 2;  // [2] an item is there
+  uint64_t *iempty_bar = ifull_bar + 2;  // [2] every warp is done with it
+  uint64_t *drain_bar = iempty_bar + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain_bar + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  static_assert(2 * sizeof(Item) + (2 * kSlots + 17) * 8 + 8 <= 512, "items, barriers and flags fit their reserve");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -198,105 +307,110 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_bar[2 * t], kSoftmaxWarps / 2);
       mbar_init(&p_bar[2 * t + 1], kSoftmaxWarps / 2);
       mbar_init(&o_bar[t], 1);
+      mbar_init(&qfull_bar[t], 1);
+      mbar_init(&qempty_bar[t], 1);
+      mbar_init(&ifull_bar[t], 1);
+      mbar_init(&iempty_bar[t], kSoftmaxWarps + 3);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
-  static_assert((2 * kSlots + 9) * 8 + 8 <= 256, "barriers and flags fit their reserve");
   if (warp == kSoftmaxWarps + 1) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  pdl_launch_dependents();
-  pdl_wait_prerequisite();
-
-  // The block's sequence and query tiles. Slot f(b) = seq_start[b] / T + b
-  // leaves sequence b room for its ceil(q / T) blocks of T tokens. Later
-  // tokens see more keys, so slots are walked from the last.
-  const int tpt = kRows / a.group, T = 2 * tpt;
-  const int64_t slot = slots_total - 1 - blockIdx.x / a.c.heads;
-  const int h = static_cast<int>(blockIdx.x % a.c.heads);
-  const auto f = [&](int32_t i) { return static_cast<int64_t>(__ldg(a.s.seq_start + i) / T) + i; };
-  const int32_t b = warp_count_le(f, a.s.batch, slot) - 1;
-  KvSeq seq = {0, 0, 0};
-  if (b >= 0) seq = load_seq(a.s, b, a.s.max_kv, a.status);
-  const int64_t tile = b >= 0 ? slot - f(b) : 0;
-  const int32_t prefix = a.prefix && b >= 0 ? __ldg(a.prefix + b) : 0;
-  const bool work = tile * T < seq.q;
-  const int tok0 = work ? static_cast<int>(tile) * T : 0;  // the block's first token in its sequence
-  const int first_pos = max(seq.pos0() + tok0, 0);
-  // Tokens of tile A (t = 0) or B, and the key tiles it walks. Both walk from
-  // the block's first key, so one walk is a prefix of the other.
-  const auto toks_of = [&](int t) { return work ? max(0, min(tpt, seq.q - tok0 - t * tpt)) : 0; };
-  const auto count_of = [&](int t) {
-    const int last = seq.pos0() + tok0 + t * tpt + toks_of(t);  // one past its last position
-    return toks_of(t) > 0 && last > 0 ? tile_walk(kKeys, prefix, seq.n, first_pos, last, a.window).count : 0;
-  };
-  const TileWalk walk = tile_walk(kKeys, prefix, seq.n, first_pos, seq.n, a.window);
-  const int count_a = count_of(0), count_b = count_of(1), most = max(count_a, count_b);
-  const int64_t krow = (static_cast<int64_t>(max(b, 0)) * a.c.heads + h) * x.len;
-
-  // Q rows into shared memory, swizzled as TMA would; zeros where there is no row
-  const int w = (warp >> 2) & 1;  // query tile of a softmax warp
-  const bool softmax = warp < kSoftmaxWarps;
-  const int row = threadIdx.x & (kRows - 1);
-  const int tok = row / a.group, hq = h * a.group + (row - tok * a.group);
-  const int my_tok0 = tok0 + w * tpt, my_toks = softmax ? toks_of(w) : 0;
-  const bool real = tok < my_toks;
-  if (softmax && work) {
-    // each warp its 32 rows, the chunks of a row by neighbouring lanes (whole
-    // sectors; a lane per row would touch 32 far rows with every load)
-#pragma unroll 4
-    for (int i = lane; i < 32 * (D / 8); i += 32) {
-      const int r = (warp & 3) * 32 + i / (D / 8), c = i % (D / 8);
-      const int r_tok = r / a.group;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r_tok < my_toks)
-        v = __ldg(reinterpret_cast<const uint4 *>(a.q.p + (seq.row0 + my_tok0 + r_tok) * a.q.token_stride +
-                                                  (h * a.group + (r - r_tok * a.group)) * a.q.head_stride) + c);
-      *reinterpret_cast<uint4 *>(sQ + w * C::kTile + r * 128 + (c >> 3) * kBox + (((c & 7) ^ (r & 7)) << 4)) = v;
-    }
-    fence_proxy_async_smem();
-  }
   tc_fence_before();
+  __syncwarp();
   __syncthreads();
   tc_fence_after();
+  pdl_launch_dependents();
+  pdl_wait_prerequisite();
   const uint32_t tmem = *tmem_slot;
+  const int tpt = kRows / a.group;  // tokens of a tile
 
-  // Ring items in the order the MMAs use them: K(0), then V(j), K(j + 1) for j = 0, 1, ...
+  // Tokens of an item's tile A (t = 0) or B, the key tiles it walks, and the
+  // walk. Both tiles walk from the item's first key, so one walk is a prefix
+  // of the other.
+  const auto toks_of = [&](const QueryBlock &q, int t) { return max(0, min(tpt, q.toks - t * tpt)); };
+  const auto count_of = [&](const QueryBlock &q, int t) {
+    const int toks = toks_of(q, t), last = q.pos + t * tpt + toks;  // one past its last position
+    return toks > 0 && last > 0 ? tile_walk(kKeys, q.prefix, q.n, max(q.pos, 0), last, a.window).count : 0;
+  };
+  const auto walk_of = [&](const QueryBlock &q) {
+    return tile_walk(kKeys, q.prefix, q.n, max(q.pos, 0), q.n, a.window);
+  };
+  // The it-th item of this block (false: there are no more, or the kernel gave up).
+  const auto take = [&](int it, Item &item, bool &ok) {
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&ifull_bar[it & 1], static_cast<uint32_t>(it >> 1) & 1u, abort_flag,
+                                                   limit_ns))) {
+      ok = false;
+      return false;
+    }
+    item = s_item[it & 1];
+    return item.q.toks > 0;
+  };
+  const auto done_with = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&iempty_bar[it & 1]);
+  };
+  const auto fail = [&]() {
+    record_error(a.status, W8A8_ERR_DEVICE_TIMEOUT);
+    *abort_flag = 1;
+  };
+
   if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kSoftmaxWarps && lane == 0 && most > 0) {
-      // ------------------------------------------------ TMA producer
-      bool ok = true;
-      int i = 0;
-      const auto load = [&](const CUtensorMap *map, int j) {
-        if (!ok) return;
-        const int s = i % kSlots;
-        if (!mbar_wait_bounded(&empty_bar[s], (static_cast<uint32_t>(i / kSlots) & 1u) ^ 1u, abort_flag, limit_ns)) {
-          ok = false;
-          return;
-        }
-        const int32_t y = static_cast<int32_t>(krow + walk.tile(j) * kKeys);
-        mbar_arrive_expect_tx(&full_bar[s], C::kTile);
+    if (warp == kSoftmaxWarps) {
+      if (lane == 0) {
+        // ------------------------------------------------ items, and their key tiles by TMA:
+        // K(0), then V(j), K(j + 1) for j = 0, 1, ..., the order in which the MMAs use them
+        bool ok = true;
+        int i = 0;  // ring items loaded
+        const int32_t items = x.counters[0] * a.c.heads;
+        const auto load = [&](const CUtensorMap *map, int64_t key) {
+          if (!ok) return;
+          const int s = i % kSlots;
+          if (!mbar_wait_bounded(&empty_bar[s], (static_cast<uint32_t>(i / kSlots) & 1u) ^ 1u, abort_flag, limit_ns)) {
+            ok = false;
+            return;
+          }
+          mbar_arrive_expect_tx(&full_bar[s], C::kTile);
 #pragma unroll
-        for (int c = 0; c < C::kAtoms; ++c) tma_load_2d(map, &full_bar[s], sKV + s * C::kTile + c * kBox, 64 * c, y);
-        ++i;
-      };
-      load(&tmK, 0);
-      for (int j = 0; j < most && ok; ++j) {
-        load(&tmV, j);
-        if (j + 1 < most) load(&tmK, j + 1);
+          for (int c = 0; c < C::kAtoms; ++c)
+            tma_load_2d(map, &full_bar[s], sKV + s * C::kTile + c * kBox, 64 * c, static_cast<int32_t>(key));
+          ++i;
+        };
+        for (int it = 0; ok; ++it) {
+          const int32_t n = atomicAdd(x.counters + 1, 1);
+          Item item = {};
+          if (n < items) {
+            item.q = x.blocks[n / a.c.heads];
+            item.h = n % a.c.heads;
+          }
+          if (!mbar_wait_bounded(&iempty_bar[it & 1], (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u, abort_flag, limit_ns)) {
+            ok = false;
+            break;
+          }
+          s_item[it & 1] = item;
+          mbar_arrive(&ifull_bar[it & 1]);
+          if (n >= items) break;
+          const TileWalk walk = walk_of(item.q);
+          const int most = max(count_of(item.q, 0), count_of(item.q, 1));
+          const int64_t key0 = (static_cast<int64_t>(item.q.b) * a.c.heads + item.h) * x.len;
+          if (most > 0) load(&tmK, key0 + walk.tile(0) * kKeys);
+          for (int j = 0; j < most && ok; ++j) {
+            load(&tmV, key0 + walk.tile(j) * kKeys);
+            if (j + 1 < most) load(&tmK, key0 + walk.tile(j + 1) * kKeys);
+          }
+        }
+        if (!ok) {
+          fail();
+          for (int n = max(0, i - kSlots); n < i; ++n)  // copies in flight land before the block leaves
+            mbar_wait_bounded(&full_bar[n % kSlots], static_cast<uint32_t>(n / kSlots) & 1u, nullptr, limit_ns / 16 + 1);
+        }
       }
-      if (!ok) {
-        record_error(a.status, W8A8_ERR_DEVICE_TIMEOUT);
-        *abort_flag = 1;
-        for (int n = max(0, i - kSlots); n < i; ++n)  // copies in flight land before the block leaves
-          mbar_wait_bounded(&full_bar[n % kSlots], static_cast<uint32_t>(n / kSlots) & 1u, nullptr, limit_ns / 16 + 1);
-      }
-    }
-    if (warp == kSoftmaxWarps + 1 && most > 0) {
+    } else if (warp == kSoftmaxWarps + 1) {
       // ------------------------------------------------ MMA issuer
       // The whole warp walks the loop, so that every operand is warp-uniform,
       // and one elected lane issues.
@@ -304,17 +418,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_lo = desc_lo_k_sw128(smem_addr(sQ)), k_lo = desc_lo_k_sw128(smem_addr(sKV)),
                      v_lo = desc_lo_mn_sw128(smem_addr(sKV), kBox);
       bool ok = true;
-      int i = 0;  // next ring item
-      const auto wait_item = [&]() {
+      int i = 0;                   // next ring item
+      uint32_t steps_a = 0, steps_b = 0;  // score tiles issued of A and B
+      const auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity & 1u, abort_flag, limit_ns));
+      };
+      const auto wait_slot = [&]() {
         const int s = i % kSlots;
-        if (ok)
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full_bar[s], static_cast<uint32_t>(i / kSlots) & 1u, abort_flag,
-                                                         limit_ns));
-        tc_fence_after();
+        wait(&full_bar[s], static_cast<uint32_t>(i / kSlots));
         ++i;
         return s;
       };
-      const auto scores = [&](int t, int slot) {  // S_t = Q_t K^T; by the elected lane
+      const auto scores = [&](int t, int slot, bool last) {  // S_t = Q_t K^T; by the elected lane
         const uint32_t qa = q_lo + t * (C::kTile / 16), ka = k_lo + slot * (C::kTile / 16);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
@@ -322,75 +437,124 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_bf16(tmem + t * kKeys, qa + off, ka + off, kIdescS, k != 0);
         }
         mma_commit(&s_bar[t]);
+        if (last) mma_commit(&qempty_bar[t]);
       };
-      const int slot0 = wait_item();
-      if (ok && elect_one()) {
-        if (count_a > 0) scores(0, slot0);
-        if (count_b > 0) scores(1, slot0);
-        mma_commit(&empty_bar[slot0]);
-      }
-      __syncwarp();
-      for (int j = 0; j < most && ok; ++j) {
-        const int v_slot = wait_item();
-        const int k_slot = j + 1 < most ? wait_item() : 0;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int count = t ? count_b : count_a;
-          if (!ok || j >= count) continue;
-          const uint32_t va = v_lo + v_slot * (C::kTile / 16);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {  // 64 keys as soon as their weights are there
-            if (ok)
-              ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&p_bar[2 * t + half], static_cast<uint32_t>(j) & 1u,
-                                                             abort_flag, limit_ns));
-            if (!ok) continue;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-              for (int k = 4 * half; k < 4 * half + 4; ++k)
-                mma_bf16_ta(tmem + kOCol + t * 128, tmem + t * kKeys + 8 * k, va + 2048 / 16 * k, kIdescO, (j | k) != 0);
-              if (half == 1) {
-                // the next scores overwrite the weights just read: the tensor core works in order
-                if (j + 1 < count)
-                  scores(t, k_slot);
-                else
-                  mma_commit(&o_bar[t]);
-              }
-            }
-            __syncwarp();
-          }
-        }
+      Item item;
+      for (int it = 0; take(it, item, ok); ++it) {
+        const int count_a = count_of(item.q, 0), count_b = count_of(item.q, 1), most = max(count_a, count_b);
+        done_with(it);
+        wait(&qfull_bar[0], static_cast<uint32_t>(it));
+        wait(&qfull_bar[1], static_cast<uint32_t>(it));
+        int slot = most > 0 ? wait_slot() : 0;
+        tc_fence_after();
         if (ok && elect_one()) {
-          mma_commit(&empty_bar[v_slot]);
-          if (j + 1 < most) mma_commit(&empty_bar[k_slot]);
+          // a tile without keys hands its query rows back at once
+          if (count_a > 0) scores(0, slot, count_a == 1); else mbar_arrive(&qempty_bar[0]);
+          if (count_b > 0) scores(1, slot, count_b == 1); else mbar_arrive(&qempty_bar[1]);
+          if (most > 0) mma_commit(&empty_bar[slot]);
         }
         __syncwarp();
+        for (int j = 0; j < most && ok; ++j) {
+          const int v_slot = wait_slot();
+          const int k_slot = j + 1 < most ? wait_slot() : 0;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int count = t ? count_b : count_a;
+            if (!ok || j >= count) continue;
+            const uint32_t parity = (t ? steps_b : steps_a) + static_cast<uint32_t>(j);
+            const uint32_t va = v_lo + v_slot * (C::kTile / 16);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // 64 keys as soon as their weights are there
+              wait(&p_bar[2 * t + half], parity);
+              if (!ok) continue;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 4 * half; k < 4 * half + 4; ++k)
+                  mma_bf16_ta(tmem + kOCol + t * 128, tmem + t * kKeys + 8 * k, va + 2048 / 16 * k, kIdescO, (j | k) != 0);
+                if (half == 1) {
+                  // the next scores overwrite the weights just read: the tensor core works in order
+                  if (j + 1 < count)
+                    scores(t, k_slot, j + 2 == count);
+                  else
+                    mma_commit(&o_bar[t]);
+                }
+              }
+              __syncwarp();
+            }
+          }
+          if (ok && elect_one()) {
+            mma_commit(&empty_bar[v_slot]);
+            if (j + 1 < most) mma_commit(&empty_bar[k_slot]);
+          }
+          __syncwarp();
+        }
+        steps_a += static_cast<uint32_t>(count_a);
+        steps_b += static_cast<uint32_t>(count_b);
       }
       if (!ok && elect_one()) {
-        record_error(a.status, W8A8_ERR_DEVICE_TIMEOUT);
-        *abort_flag = 1;
+        fail();
         mma_commit(drain_bar);  // MMAs in flight finish before TMEM is freed
         mbar_wait_bounded(drain_bar, 0, nullptr, limit_ns / 16 + 1);
       }
       __syncwarp();
+    } else {
+      // ------------------------------------------------ query rows, a warp to a tile
+      const int t = warp - (kSoftmaxWarps + 2);
+      const uint32_t dst = smem_addr(sQ + t * C::kTile);
+      bool ok = true;
+      Item item;
+      for (int it = 0; take(it, item, ok); ++it) {
+        const int toks = toks_of(item.q, t), row0 = item.q.row + t * tpt, h0 = item.h * a.group;
+        done_with(it);
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&qempty_bar[t], (static_cast<uint32_t>(it) & 1u) ^ 1u, abort_flag,
+                                                       limit_ns))) {
+          ok = false;
+          break;
+        }
+        // swizzled as TMA would, the chunks of a row by neighbouring lanes; zeros where there is no row
+#pragma unroll 4
+        for (int n = lane; n < kRows * (D / 8); n += 32) {
+          const int r = n / (D / 8), c = n % (D / 8);
+          const int tok = r / a.group;
+          const bool real = tok < toks;
+          const uint16_t *src = a.q.p + (real ? (row0 + tok) * a.q.token_stride + (h0 + r - tok * a.group) * a.q.head_stride + 8 * c : 0);
+          cp_async16_zfill(dst + r * 128 + (c >> 3) * kBox + (((c & 7) ^ (r & 7)) << 4), src, real);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qfull_bar[t]);
+      }
+      if (!ok && lane == 0) fail();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    if (work) {
     // -------------------------------------------------- softmax
-    const int count = w ? count_b : count_a;
+    const int w = warp >> 2;  // query tile
+    const int row = threadIdx.x & (kRows - 1), tok = row / a.group;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + static_cast<uint32_t>(w * kKeys);
     const uint32_t t_o = tmem + lanes + kOCol + static_cast<uint32_t>(w * 128);
-    const int pos = real ? seq.pos0() + my_tok0 + tok : -1;
-    const int pos_min = seq.pos0() + my_tok0, pos_max = pos_min + my_toks - 1;
+    uint8_t *const stage = sStage + warp * kStage;
     const bool cap = a.softcap > 0.0f;
     const float mul = cap ? a.scale / a.softcap : a.scale * kLog2e;
     const float cap2 = a.softcap * kLog2e;
-    const float slope = a.slopes && real ? __ldg(a.slopes + hq) * kLog2e : 0.0f;
     const bool plain = !cap && !a.slopes && a.scale >= 0.0f;  // a granule's largest score is its largest product
-    float m = -INFINITY, l = 0.0f;
     bool ok = true;
+    uint32_t steps = 0, outs = 0;  // score tiles and outputs of this query tile so far
+    Item item;
+    for (int it = 0; take(it, item, ok); ++it) {
+    const int toks = toks_of(item.q, w), count = count_of(item.q, w), n = item.q.n, prefix = item.q.prefix;
+    const TileWalk walk = walk_of(item.q);
+    const int row0 = item.q.row + w * tpt, h0 = item.h * a.group;
+    const int pos_min = item.q.pos + w * tpt, pos_max = pos_min + toks - 1;
+    const int64_t krow = (static_cast<int64_t>(item.q.b) * a.c.heads + item.h) * x.len;
+    done_with(it);
+    const bool real = tok < toks;
+    const int pos = real ? pos_min + tok : -1;
+    const float slope = a.slopes && real ? __ldg(a.slopes + h0 + row - tok * a.group) * kLog2e : 0.0f;
+    float m = -INFINITY, l = 0.0f;
     const float *ks = x.ks + krow / kGran, *vs = x.vs + krow / kGran;
     for (int j = 0; j < count; ++j) {
       const int key0 = walk.tile(j) * kKeys;
@@ -405,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool whole = key0 + kKeys - 1 <= pos_min && (a.window == 0 || key0 > pos_max - a.window);
 #pragma unroll
       for (int g = 0; g < 8; ++g) whole = whole && kc[g] != -1.0f;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&s_bar[w], static_cast<uint32_t>(j) & 1u, abort_flag, limit_ns))) {
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&s_bar[w], (steps + static_cast<uint32_t>(j)) & 1u, abort_flag, limit_ns))) {
         ok = false;
         break;
       }
@@ -439,9 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {  // element by element
         const float far = slope * static_cast<float>(key0 - pos);
         // keys key0 + e of this row: e <= hi and e >= lo, or e < pre
-        const int hi = pos < 0 ? -1 : min(pos, seq.n - 1) - key0;
+        const int hi = pos < 0 ? -1 : min(pos, n - 1) - key0;
         const int lo = a.window > 0 ? pos - a.window + 1 - key0 : -key0;
-        const int pre = pos < 0 ? 0 : min(prefix, seq.n) - key0;
+        const int pre = pos < 0 ? 0 : min(prefix, n) - key0;
         // CAP: tanh cap; BIAS: distance bias; MASK: some row of the tile does
         // not see some key (CAP decides about the other two as it goes)
         const auto finish = [&](auto cap_c, auto bias_c, auto mask_c, uint32_t(&s)[32], int c) {
@@ -565,54 +729,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       l += (l0 + l1) + (l2 + l3);
     }
     if (ok && count > 0)
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&o_bar[w], 0, abort_flag, limit_ns));
-    if (!ok) {
-      if (lane == 0) {
-        record_error(a.status, W8A8_ERR_DEVICE_TIMEOUT);
-        *abort_flag = 1;
-      }
-    } else {
-      tc_fence_after();
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      // rows through the query tile's memory (its last product is complete), then out by neighbouring lanes
-      uint8_t *const stage = sQ + w * C::kTile;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&o_bar[w], outs & 1u, abort_flag, limit_ns));
+    if (!ok) break;
+    tc_fence_after();
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float r_out = a.r_out ? __ldg(a.r_out) : 0.0f;
+    const int z_out = a.r_out ? __ldg(a.z_out) : 0;
+    // 64 dims of the warp's 32 rows at a time through its staging, then out by neighbouring lanes
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
+    for (int part = 0; part < C::kAtoms; ++part) {
+      constexpr int kMost = 64;
+      const int dims = D - kMost * part < kMost ? D - kMost * part : kMost;
+#pragma unroll
+      for (int c = 0; c < kMost / 16; ++c) {
+        if (16 * c >= dims) continue;
         uint32_t o[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[e] = 0;
         if (count > 0) {
-          tmem_ld_32x32b_x16(t_o + 16 * c, o);
+          tmem_ld_32x32b_x16(t_o + kMost * part + 16 * c, o);
           tmem_ld_wait();
         }
         uint32_t y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           y[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-        uint8_t *const at = stage + row * 128 + (c >> 2) * kBox;
-        const int c0 = (2 * c) & 7;
-        *reinterpret_cast<uint4 *>(at + ((c0 ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<uint4 *>(at + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+        uint8_t *const at = stage + lane * kStageRow;
+        *reinterpret_cast<uint4 *>(at + (((2 * c) ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4 *>(at + (((2 * c + 1) ^ (lane & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
       }
       __syncwarp();
-      const float r_out = a.r_out ? __ldg(a.r_out) : 0.0f;
-      const int z_out = a.r_out ? __ldg(a.z_out) : 0;
+      const int chunks = dims / 8;
 #pragma unroll 4
-      for (int i = lane; i < 32 * (D / 8); i += 32) {
-        const int r = (warp & 3) * 32 + i / (D / 8), c = i % (D / 8);
+      for (int i = lane; i < 32 * chunks; i += 32) {
+        const int r1 = i / chunks, c = i - r1 * chunks, r = (warp & 3) * 32 + r1;
         const int r_tok = r / a.group;
-        if (r_tok >= my_toks) continue;
-        const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 128 + (c >> 3) * kBox + (((c & 7) ^ (r & 7)) << 4));
-        const int64_t elem = (static_cast<int64_t>(seq.row0 + my_tok0 + r_tok) * a.q_heads + h * a.group +
-                              (r - r_tok * a.group)) * D + 8 * c;
+        if (r_tok >= toks) continue;
+        const uint4 v = *reinterpret_cast<const uint4 *>(stage + r1 * kStageRow + ((c ^ (r1 & 7)) << 4));
+        const int64_t elem =
+            (static_cast<int64_t>(row0 + r_tok) * a.q_heads + h0 + r - r_tok * a.group) * D + kMost * part + 8 * c;
         if (!a.r_out)
           *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + elem) = v;
         else
           *reinterpret_cast<uint2 *>(static_cast<int8_t *>(a.out) + elem) = quant8_asym_sat(v, r_out, z_out);
       }
+      __syncwarp();
     }
+    tc_fence_before();  // O has been read before this warp's next weights let it be overwritten
+    steps += static_cast<uint32_t>(count);
+    outs += count > 0 ? 1u : 0u;
     }
+    if (!ok && lane == 0) fail();
   }
+
   tc_fence_before();
   __syncwarp();  // lanes of the producer and MMA warps reconverge before the CTA barrier
   __syncthreads();
@@ -622,20 +791,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+int64_t query_block_slots(const KvAttnArgs &a) { return a.s.tokens / (2 * (kRows / a.group)) + a.s.batch; }
+
 Expanded expanded_of(const KvAttnArgs &a, void *workspace) {
   Expanded x;
   x.len = expanded_len(a.s.max_kv);
+  x.slots = static_cast<int32_t>(query_block_slots(a));
   const int64_t keys = static_cast<int64_t>(a.s.batch) * a.c.heads * x.len;
   const int64_t pitch = a.c.d > 64 ? 128 : 64;
   x.k = static_cast<uint16_t *>(workspace);
   x.v = x.k + keys * pitch;
   x.ks = reinterpret_cast<float *>(x.v + keys * pitch);
   x.vs = x.ks + keys / kGran;
+  x.blocks = reinterpret_cast<QueryBlock *>(x.vs + keys / kGran);
+  x.counters = reinterpret_cast<int32_t *>(x.blocks + x.slots);
   return x;
 }
 
 template <int D>
-cudaError_t launch_t(const KvAttnArgs &a, void *workspace, cudaStream_t s) {
+cudaError_t launch_t(const KvAttnArgs &a, void *workspace, int num_sms, cudaStream_t s) {
   using C = PCfg<D>;
   const Expanded x = expanded_of(a, workspace);
   cudaLaunchConfig_t cfg = {};
@@ -647,44 +821,41 @@ cudaError_t launch_t(const KvAttnArgs &a, void *workspace, cudaStream_t s) {
   cfg.stream = s;
   alignas(64) CUtensorMap tmK = {}, tmV = {};  // not used where no sequence has a key
   const uint64_t rows = static_cast<uint64_t>(a.s.batch) * a.c.heads * x.len;
-  if (rows > 0) {
-    if (!encode_tmap_2d(&tmK, x.k, TmapType::kBF16, C::kPitch, rows, C::kPitch * 2, 64, kKeys, true) ||
-        !encode_tmap_2d(&tmV, x.v, TmapType::kBF16, C::kPitch, rows, C::kPitch * 2, 64, kKeys, true))
-      return cudaErrorInvalidValue;
-    cfg.gridDim = dim3(static_cast<unsigned>(x.len / kExpandKeys), a.c.heads, a.s.batch);
-    cfg.blockDim = dim3(kExpandThreads);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kv_expand_kernel<D>, a, x);
-    if (e != cudaSuccess) return e;
-  }
-  cudaError_t e = ensure_kernel_smem<kv_prefill_kernel<D>>(static_cast<int>(C::kSmem), false);
+  if (rows > 0 && (!encode_tmap_2d(&tmK, x.k, TmapType::kBF16, C::kPitch, rows, C::kPitch * 2, 64, kKeys, true) ||
+                   !encode_tmap_2d(&tmV, x.v, TmapType::kBF16, C::kPitch, rows, C::kPitch * 2, 64, kKeys, true)))
+    return cudaErrorInvalidValue;
+  cfg.gridDim = dim3(static_cast<unsigned>(1 + x.len / kExpandKeys), a.c.heads, a.s.batch);
+  cfg.blockDim = dim3(kExpandThreads);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_expand_kernel<D>, a, x);
   if (e != cudaSuccess) return e;
-  const int T = 2 * (kRows / a.group);
-  const int64_t slots = a.s.tokens / T + a.s.batch;
-  cfg.gridDim = dim3(static_cast<unsigned>(slots * a.c.heads));
+  e = ensure_kernel_smem<kv_prefill_kernel<D>>(static_cast<int>(C::kSmem), false);
+  if (e != cudaSuccess) return e;
+  const int64_t items = static_cast<int64_t>(x.slots) * a.c.heads;
+  cfg.gridDim = dim3(static_cast<unsigned>(items < num_sms ? items : num_sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
-  return cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D>, tmK, tmV, a, x, slots, kWaitLimitNs);
+  return cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D>, tmK, tmV, a, x, kWaitLimitNs);
 }
 
 }  // namespace
 
 bool kv_prefill_fits(const KvAttnArgs &a) {
-  // rows of the expanded matrices are int32 tensor-map coordinates, slots x heads a grid
+  // rows of the expanded matrices are int32 tensor-map coordinates, items an int32 count
   const int64_t rows = static_cast<int64_t>(a.s.batch) * a.c.heads * expanded_len(a.s.max_kv);
-  const int64_t blocks = (a.s.tokens / (2 * (kRows / a.group)) + a.s.batch) * a.c.heads;
-  return rows <= INT32_MAX && blocks <= INT32_MAX;
+  return rows <= INT32_MAX && query_block_slots(a) * a.c.heads <= INT32_MAX / 2;
 }
 
 size_t kv_prefill_workspace_bytes(const KvAttnArgs &a) {
   const size_t keys = static_cast<size_t>(a.s.batch) * a.c.heads * expanded_len(a.s.max_kv);
-  return keys * ((a.c.d > 64 ? 128 : 64) * 2 * sizeof(uint16_t)) + keys / kGran * 2 * sizeof(float);
+  return keys * ((a.c.d > 64 ? 128 : 64) * 2 * sizeof(uint16_t)) + keys / kGran * 2 * sizeof(float) +
+         static_cast<size_t>(query_block_slots(a)) * sizeof(QueryBlock) + 16;
 }
 
-cudaError_t launch_kv_prefill(const KvAttnArgs &a, void *workspace, cudaStream_t s) {
+cudaError_t launch_kv_prefill(const KvAttnArgs &a, void *workspace, int num_sms, cudaStream_t s) {
   switch (a.c.d) {
-    case 64: return launch_t<64>(a, workspace, s);
-    case 96: return launch_t<96>(a, workspace, s);
-    case 128: return launch_t<128>(a, workspace, s);
+    case 64: return launch_t<64>(a, workspace, num_sms, s);
+    case 96: return launch_t<96>(a, workspace, num_sms, s);
+    case 128: return launch_t<128>(a, workspace, num_sms, s);
     default: return cudaErrorInvalidValue;
   }
 }
