@@ -551,7 +551,7 @@ typedef struct w8a8_kv_scores {
  * kv_heads) <= 32 (relative error 2^-16), and once beyond (2^-8 each, the
  * error of a sum of n such terms growing like sqrt(n) against n).
  *   q      device bf16 [tokens, q_heads, head_dim], strides in elements
- *          (multiples of 8)
+ *          (multiples of 8, and not 0 where the axis has several elements)
  *   out    device bf16 [tokens, q_heads, head_dim] dense, 16-byte aligned
  *   workspace  device, >= w8a8_kv_attention_workspace_size(...) bytes,
  *          16-byte aligned; no initial contents needed, and calls that may

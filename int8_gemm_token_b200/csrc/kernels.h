@@ -199,5 +199,9 @@ w8a8_status current_device_info(int *sm_count, int32_t **status_word);
 enum class TmapType { kU8, kBF16, kF32 };
 bool encode_tmap_2d(void *map, const void *base, TmapType type, uint64_t inner, uint64_t outer,
                     uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer, bool swizzle128);
+// 3-D tensor map of bf16 values, 128-byte swizzle (box0 is 64): extents and
+// box in elements, strides of axes 1 and 2 in bytes.
+bool encode_tmap_3d_bf16(void *map, const void *base, uint64_t n0, uint64_t n1, uint64_t n2, uint64_t stride1,
+                         uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2);
 
 }  // namespace w8a8

@@ -117,6 +117,7 @@ w8a8_status run_attention(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch
   if (!aligned(scores->slopes, 4) || !aligned(scores->prefix_len, 4)) return W8A8_ERR_MISALIGNED;
   if (tokens == 0 || a.s.batch == 0 || a.s.max_q == 0) return W8A8_OK;
   if (w8a8_status s = check_rows(q, q_token_stride, q_head_stride, &a.q)) return s;
+  if ((tokens > 1 && q_token_stride == 0) || (q_heads > 1 && q_head_stride == 0)) return W8A8_ERR_INVALID_ARG;
   if (!out) return W8A8_ERR_INVALID_ARG;
   if (!aligned(out, 16) || !aligned(workspace, 16)) return W8A8_ERR_MISALIGNED;
   a.scale = scores->scale;

@@ -21,15 +21,17 @@
 //                 operand of the second product (over S, which is dead by
 //                 then); at the end O / l to global memory, through shared
 //                 memory so that neighbouring lanes store neighbouring bytes;
-//     warp 8      takes items and loads 128-byte-swizzled 128 x 64 boxes of
-//                 K and V (TMA) into a ring of key tiles;
+//     warp 8      takes items and loads 128-byte-swizzled boxes of 64 dims by
+//                 TMA: key tiles of K and V into a ring;
 //     warp 9      MMA issuer: S = Q K^T (both K-major in shared memory) and
 //                 O += P V (P in TMEM, V as an MN-major operand, so V needs
 //                 no transpose). While one tile's softmax runs, the other
 //                 tile's products do; the next item's first scores are
 //                 computed while this one's output is written;
-//     warps 10, 11  load the next item's query rows (cp.async) as soon as the
-//                 last scores of this one are done.
+//     warp 10     loads the next item's query rows as soon as the last scores
+//                 of this one are done, as boxes of floor(128 / group) tokens x
+//                 group heads of the packed queries, which lie in shared
+//                 memory in the row order of a tile.
 //   The page scales never touch the operands: k's multiplies the scores (a
 //   granule's maximum is scaled once, an element's factor is that of the
 //   fused multiply-add before 2^x), v's multiplies the weights.
@@ -51,7 +53,7 @@ constexpr int kRows = 128;             // query rows of a tile = TMEM lanes
 constexpr int kBox = kKeys * 128;      // bytes of a 64-dim box of 128 rows
 constexpr int kSlots = 4;              // key tiles (K or V) in flight
 constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // softmax, key tiles, MMA, two for query rows
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // softmax, key tiles, MMA, query rows, one idle
 constexpr int kStageRow = 128;         // bytes of a row in a softmax warp's output staging (64 dims)
 constexpr int kStage = 32 * kStageRow;
 // Registers a thread: 168 at launch (65536 / 384); a softmax thread holds a
@@ -201,20 +203,28 @@ __global__ void __launch_bounds__(kExpandThreads) kv_expand_kernel(const __grid_
     x.vs[at] = vs;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < kExpandKeys * CH; i += kExpandThreads) {
-    const int r = i / CH, c = i - r * CH;
+  constexpr int N = (kExpandKeys * CH + kExpandThreads - 1) / kExpandThreads;
+  uint4 kv[N][2];  // every load of the thread in flight before the first is used
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int i = n * kExpandThreads + threadIdx.x, r = i / CH, c = i - r * CH;
+    kv[n][0] = kv[n][1] = make_uint4(0, 0, 0, 0);
+    if (r >= kExpandKeys) continue;
     const int key = key0 + r;
     const int32_t page = s_page[r / kGran];
-    uint4 kv[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (page >= 0 && key < seq.n) {
-      const int64_t src =
-          (((static_cast<int64_t>(page) * a.c.heads + h) << a.c.page_shift) + (key & (a.c.page - 1))) * D + 16 * c;
-      kv[0] = __ldg(reinterpret_cast<const uint4 *>(a.c.k + src));
-      kv[1] = __ldg(reinterpret_cast<const uint4 *>(a.c.v + src));
-    }
+    if (page < 0 || key >= seq.n) continue;
+    const int64_t src =
+        (((static_cast<int64_t>(page) * a.c.heads + h) << a.c.page_shift) + (key & (a.c.page - 1))) * D + 16 * c;
+    kv[n][0] = __ldg(reinterpret_cast<const uint4 *>(a.c.k + src));
+    kv[n][1] = __ldg(reinterpret_cast<const uint4 *>(a.c.v + src));
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int i = n * kExpandThreads + threadIdx.x, r = i / CH, c = i - r * CH;
+    if (r >= kExpandKeys) continue;
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-      const uint32_t w[4] = {kv[z].x, kv[z].y, kv[z].z, kv[z].w};
+      const uint32_t w[4] = {kv[n][z].x, kv[n][z].y, kv[n][z].z, kv[n][z].w};
       uint32_t o[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) codes_to_bf16(w[e], o[2 * e], o[2 * e + 1]);
@@ -262,13 +272,10 @@ struct Item {
   int32_t h, pad[3];
 };
 
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv_prefill_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+    kv_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmOut,
                       const __grid_constant__ KvAttnArgs a, const __grid_constant__ Expanded x, uint64_t limit_ns) {
   using C = PCfg<D>;
   constexpr int KS = D / 16;
@@ -294,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmQ);
     if (x.len > 0) {
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
@@ -310,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&qfull_bar[t], 1);
       mbar_init(&qempty_bar[t], 1);
       mbar_init(&ifull_bar[t], 1);
-      mbar_init(&iempty_bar[t], kSoftmaxWarps + 3);
+      mbar_init(&iempty_bar[t], kSoftmaxWarps + 2);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -498,35 +506,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_bounded(drain_bar, 0, nullptr, limit_ns / 16 + 1);
       }
       __syncwarp();
-    } else {
-      // ------------------------------------------------ query rows, a warp to a tile
-      const int t = warp - (kSoftmaxWarps + 2);
-      const uint32_t dst = smem_addr(sQ + t * C::kTile);
+    } else if (warp == kSoftmaxWarps + 2) {
+      // ------------------------------------------------ query rows
       bool ok = true;
+      int it = 0;
       Item item;
-      for (int it = 0; take(it, item, ok); ++it) {
-        const int toks = toks_of(item.q, t), row0 = item.q.row + t * tpt, h0 = item.h * a.group;
+      for (; take(it, item, ok); ++it) {
         done_with(it);
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&qempty_bar[t], (static_cast<uint32_t>(it) & 1u) ^ 1u, abort_flag,
-                                                       limit_ns))) {
-          ok = false;
-          break;
+        if (lane == 0) {
+          // Rows of tokens past the item's (another sequence's, or zeros past
+          // the last) and the rows past floor(128 / group) x group are no
+          // one's: their scores go nowhere.
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (!mbar_wait_bounded(&qempty_bar[t], (static_cast<uint32_t>(it) & 1u) ^ 1u, abort_flag, limit_ns)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&qfull_bar[t], static_cast<uint32_t>(C::kAtoms * tpt * a.group * 128));
+#pragma unroll
+            for (int c = 0; c < C::kAtoms; ++c)
+              tma_load_3d(&tmQ, &qfull_bar[t], sQ + t * C::kTile + c * kBox, 64 * c, item.h * a.group,
+                          item.q.row + t * tpt);
+          }
         }
-        // swizzled as TMA would, the chunks of a row by neighbouring lanes; zeros where there is no row
-#pragma unroll 4
-        for (int n = lane; n < kRows * (D / 8); n += 32) {
-          const int r = n / (D / 8), c = n % (D / 8);
-          const int tok = r / a.group;
-          const bool real = tok < toks;
-          const uint16_t *src = a.q.p + (real ? (row0 + tok) * a.q.token_stride + (h0 + r - tok * a.group) * a.q.head_stride + 8 * c : 0);
-          cp_async16_zfill(dst + r * 128 + (c >> 3) * kBox + (((c & 7) ^ (r & 7)) << 4), src, real);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&qfull_bar[t]);
+        ok = __shfl_sync(0xFFFFFFFFu, static_cast<int>(ok), 0) != 0;
+        if (!ok) break;
       }
-      if (!ok && lane == 0) fail();
+      if (!ok && lane == 0) {
+        fail();
+        for (int t = 0; t < 2; ++t)  // copies in flight land before the block leaves
+          for (int n = max(0, it - 1); n <= it; ++n)
+            mbar_wait_bounded(&qfull_bar[t], static_cast<uint32_t>(n) & 1u, nullptr, limit_ns / 16 + 1);
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -735,34 +746,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     const float r_out = a.r_out ? __ldg(a.r_out) : 0.0f;
     const int z_out = a.r_out ? __ldg(a.z_out) : 0;
-    // 64 dims of the warp's 32 rows at a time through its staging, then out by neighbouring lanes
+    // 64 dims of the warp's 32 rows at a time through its staging (swizzled as
+    // TMA would). bf16 rows of whole tokens that are all the item's leave as
+    // one tensor store, which the warp does not wait for; others by
+    // neighbouring lanes.
+    const bool tensor_store = !a.r_out && 32 % a.group == 0 && (warp & 3) * 32 + 32 <= toks * a.group;
 #pragma unroll
     for (int part = 0; part < C::kAtoms; ++part) {
       constexpr int kMost = 64;
       const int dims = D - kMost * part < kMost ? D - kMost * part : kMost;
+      uint32_t o4[kMost / 16][16];
 #pragma unroll
       for (int c = 0; c < kMost / 16; ++c) {
         if (16 * c >= dims) continue;
-        uint32_t o[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = 0;
         if (count > 0) {
-          tmem_ld_32x32b_x16(t_o + kMost * part + 16 * c, o);
-          tmem_ld_wait();
+          tmem_ld_32x32b_x16(t_o + kMost * part + 16 * c, o4[c]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o4[c][e] = 0;
         }
+      }
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < kMost / 16; ++c) {
+        if (16 * c >= dims) continue;
+        const uint32_t(&o)[16] = o4[c];
         uint32_t y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           y[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
         uint8_t *const at = stage + lane * kStageRow;
+        if (c == 0) {  // the staging's last store has read it
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+        }
         *reinterpret_cast<uint4 *>(at + (((2 * c) ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
         *reinterpret_cast<uint4 *>(at + (((2 * c + 1) ^ (lane & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
       }
+      if (tensor_store) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&tmOut, stage, kMost * part, h0, row0 + (warp & 3) * (32 / a.group));
+          bulk_commit_group();
+        }
+        continue;
+      }
       __syncwarp();
       const int chunks = dims / 8;
-#pragma unroll 4
-      for (int i = lane; i < 32 * chunks; i += 32) {
-        const int r1 = i / chunks, c = i - r1 * chunks, r = (warp & 3) * 32 + r1;
+#pragma unroll
+      for (int k = 0; k < kMost / 8; ++k) {
+        if (k >= chunks) continue;
+        const int i = k * 32 + lane, r1 = i / chunks, c = i - r1 * chunks, r = (warp & 3) * 32 + r1;
         const int r_tok = r / a.group;
         if (r_tok >= toks) continue;
         const uint4 v = *reinterpret_cast<const uint4 *>(stage + r1 * kStageRow + ((c ^ (r1 & 7)) << 4));
@@ -779,6 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     steps += static_cast<uint32_t>(count);
     outs += count > 0 ? 1u : 0u;
     }
+    if (lane == 0) bulk_wait_all();  // every store of this warp has completed before the block leaves
+    __syncwarp();
     if (!ok && lane == 0) fail();
   }
 
@@ -819,7 +856,18 @@ cudaError_t launch_t(const KvAttnArgs &a, void *workspace, int num_sms, cudaStre
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = s;
-  alignas(64) CUtensorMap tmK = {}, tmV = {};  // not used where no sequence has a key
+  alignas(64) CUtensorMap tmQ, tmK = {}, tmV = {}, tmOut = {};  // K and V are not used where no sequence has a key
+  // a stride of an axis of one element is never used, but must be one
+  const uint64_t row = static_cast<uint64_t>(D) * 2;
+  if (!encode_tmap_3d_bf16(&tmQ, a.q.p, D, a.q_heads, static_cast<uint64_t>(a.s.tokens),
+                           a.q_heads > 1 ? static_cast<uint64_t>(a.q.head_stride) * 2 : row,
+                           a.s.tokens > 1 ? static_cast<uint64_t>(a.q.token_stride) * 2 : row, 64,
+                           static_cast<uint32_t>(a.group), static_cast<uint32_t>(kRows / a.group)))
+    return cudaErrorInvalidValue;
+  if (!a.r_out && 32 % a.group == 0 &&
+      !encode_tmap_3d_bf16(&tmOut, a.out, D, a.q_heads, static_cast<uint64_t>(a.s.tokens), row, row * a.q_heads, 64,
+                           static_cast<uint32_t>(a.group), static_cast<uint32_t>(32 / a.group)))
+    return cudaErrorInvalidValue;
   const uint64_t rows = static_cast<uint64_t>(a.s.batch) * a.c.heads * x.len;
   if (rows > 0 && (!encode_tmap_2d(&tmK, x.k, TmapType::kBF16, C::kPitch, rows, C::kPitch * 2, 64, kKeys, true) ||
                    !encode_tmap_2d(&tmV, x.v, TmapType::kBF16, C::kPitch, rows, C::kPitch * 2, 64, kKeys, true)))
@@ -834,7 +882,7 @@ cudaError_t launch_t(const KvAttnArgs &a, void *workspace, int num_sms, cudaStre
   cfg.gridDim = dim3(static_cast<unsigned>(items < num_sms ? items : num_sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
-  return cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D>, tmK, tmV, a, x, kWaitLimitNs);
+  return cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D>, tmQ, tmK, tmV, tmOut, a, x, kWaitLimitNs);
 }
 
 }  // namespace

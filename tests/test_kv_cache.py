@@ -92,6 +92,7 @@ def test_attention_refusals():
     assert attention(scores=(1.0, 0.0, P + 1, 0, None)) == 2 and attention(scores=(1.0, 0.0, None, 0, P + 2)) == 2
     assert attention(q=None) == 1 and attention(out=None) == 1
     assert attention(q=ODD) == 2 and attention(out=ODD) == 2 and attention(ws=ODD) == 2 and attention(qh=12) == 2
+    assert attention(qt=0) == 1 and attention(qh=0) == 1  # a broadcast axis
     assert attention(tokens=0, q=None, out=None) == 0 and attention(b=batch(batch=0)) == 0
     f = W.lib().w8a8_kv_attention_requant
     s = ctypes.byref(W._ScoresStruct(1.0, 0.0, None, 0, None))
