@@ -545,11 +545,11 @@ typedef struct w8a8_kv_scores {
  *   out[t, h] = sum_j softmax(s)_j v_j       (0 for a padding row, p < 0)
  * k_j and v_j are the values the codes stand for; scores, the running maximum
  * and sum and the accumulation are fp32. Rounding: the codes enter the tensor
- * cores exactly (an int8 code is exact in bf16) and the page's scales are
- * applied in fp32. The weights times v's scale are rounded to bf16 for the
- * second product: as a high and a low part where max_q_len * (q_heads /
- * kv_heads) <= 32 (relative error 2^-16), and once beyond (2^-8 each, the
- * error of a sum of n such terms growing like sqrt(n) against n).
+ * cores exactly (an int8 code is exact in fp16 and in bf16) and so does q; the
+ * page's scales are applied in fp32. The weights times v's scale are rounded
+ * once for the second product: where max_q_len * (q_heads / kv_heads) <= 32 to
+ * fp16 against the row's largest (2^-11 of the value, at least 2^-25 of the
+ * largest), beyond to bf16 (2^-8 of the value).
  *   q      device bf16 [tokens, q_heads, head_dim], strides in elements
  *          (multiples of 8, and not 0 where the axis has several elements)
  *   out    device bf16 [tokens, q_heads, head_dim] dense, 16-byte aligned

@@ -183,6 +183,7 @@ struct KvAttnArgs {
   const int32_t *z_out = nullptr;
   int32_t *status = nullptr;
 };
+bool kv_decode_fits(const KvAttnArgs &a);
 size_t kv_decode_workspace_bytes(const KvAttnArgs &a, int num_sms);
 cudaError_t launch_kv_decode(const KvAttnArgs &a, void *workspace, int num_sms, cudaStream_t s);
 bool kv_prefill_fits(const KvAttnArgs &a);

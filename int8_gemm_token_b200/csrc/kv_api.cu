@@ -97,7 +97,7 @@ w8a8_status check_attention_shape(const w8a8_kv_cache *cache, const w8a8_kv_batc
   if (q_heads % a->c.heads != 0 || q_heads / a->c.heads > kMaxGroup) return W8A8_ERR_UNSUPPORTED_SHAPE;
   a->q_heads = q_heads;
   a->group = q_heads / a->c.heads;
-  if (!few_rows(*a) && !kv_prefill_fits(*a)) return W8A8_ERR_UNSUPPORTED_SHAPE;
+  if (few_rows(*a) ? !kv_decode_fits(*a) : !kv_prefill_fits(*a)) return W8A8_ERR_UNSUPPORTED_SHAPE;
   return W8A8_OK;
 }
 

@@ -97,7 +97,16 @@ __device__ __forceinline__ TileWalk tile_walk(int tile, int prefix, int n, int f
   return w;
 }
 
-// Final value of one output element.
+// Final values of neighbouring output elements.
+__device__ __forceinline__ void store_out2(const KvAttnArgs &a, int64_t elem, float y0, float y1) {
+  const uint32_t b = pack_bf16x2(y0, y1);
+  if (!a.r_out) {
+    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + elem) = b;
+    return;
+  }
+  const uint2 q = quant8_asym_sat(make_uint4(b, 0, 0, 0), __ldg(a.r_out), __ldg(a.z_out));
+  *reinterpret_cast<uint16_t *>(static_cast<int8_t *>(a.out) + elem) = static_cast<uint16_t>(q.x);
+}
 __device__ __forceinline__ void store_out4(const KvAttnArgs &a, int64_t elem, const float (&y)[4]) {
   const uint2 b = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
   if (!a.r_out) {

@@ -8,42 +8,63 @@
 // with scores in units of log2.
 //
 // How: the bound is the cache's bytes from HBM, each used once for all the
-// query rows of its kv head, so a warp takes 32 keys at a time and the rows
+// query rows of its kv head, so a warp takes 16 keys at a time and the rows
 // (group * new tokens) are the narrow side of the products: S^T = K Q^T with
 // 16 keys x 8 rows x 16 dims an instruction, and O^T = V^T P^T with 16 dims x
 // 8 rows x 16 keys. Those shapes are mma.sync's; tcgen05 wants 128 rows of
-// one operand in shared memory as bf16, which the int8 codes are not until a
-// register has held them. Codes become bf16 in registers, exactly:
-// bf16(128 + (q & 127)) - bf16(128 or 256, by q's sign), both bit patterns
-// made by masking a byte into 0x43xx.
+// one operand in shared memory as fp16, which the int8 codes are not until a
+// register has held them. Codes become fp16 in registers, exactly: the byte
+// q + 128 under 0x64 is the bit pattern of 1024 + 128 + q, from which 1152 is
+// subtracted (per four codes one xor, two byte permutes, two packed adds).
+//   fp16 has the codes' bits to spare but not bf16's range, so what meets them
+// is scaled by powers of two, exactly: a query row so that its largest
+// element is in [2^14, 2^15) (elements 2^-29 below it start to lose bits), and
+// the weights 2^s_j times v's scale against their own running maximum, apart
+// from that of the scores:
+//   mv = max_j (s_j + log2 vs_j),  w_j = 2^(s_j + log2 vs_j - mv) <= 1,
+//   out = 2^(mv - m) (sum_j w_j code_j) / l,  l = sum_j 2^(s_j - m) in fp32.
+// w_j is rounded to fp16 once (2^-11).
 //   Both contractions may run over their axis in any order as long as both
 // sides use the same one, so a lane reads its codes of K as 16 contiguous
 // bytes of one key and those of V as the same dims of four keys (pairs of
-// keys are interleaved by byte permutes), and P goes from the accumulator
+// keys are interleaved by byte permutes), and w goes from the accumulator
 // layout of the first product to the operand layout of the second by an 8x8
-// transpose (movmatrix). P times the page's v scale enters as bf16 high part
-// plus bf16 low part.
+// transpose (movmatrix).
 //   Loads are 16-byte cp.async into a ring of each warp's own, so a warp
 // waits for nobody; the stages are swizzled so that both reads are free of
 // bank conflicts (D = 128).
+//
+// Work: the key tiles (16 keys) of all segments -- (sequence, kv head, block
+// of query rows) -- laid end to end, each with kSetup units more for its
+// start, are cut into equal pieces, one to a warp, whatever the lengths of
+// the sequences, which only the device knows. A warp that holds all of a
+// segment writes its output; parts go to the workspace (sums, maxima, sum of
+// weights) and kv_join_kernel joins them in the order of the pieces. The same
+// arithmetic on the lengths tells it who has what.
 #include "kv_common.cuh"
 
 namespace w8a8 {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 32;    // keys of a warp's tile
-constexpr int kStages = 3;
-constexpr int kPagesAhead = 16;  // tiles whose pages and scales a warp holds, two granules each, one per lane
+constexpr int kTile = kGran;  // keys of a tile: one MMA's, of one page
+constexpr int kSetup = 4;     // what a segment's start costs, in tiles
+constexpr int kMinUnits = 8;  // of a piece
+constexpr int kJoinWarps = 4;
 
-template <int D>
+// Blocks of an SM and stages of a warp's ring: with 8 query rows 16 warps of
+// 128 registers, with 16 rows (twice the sums and queries in registers) 12.
+template <int D, int NT>
 struct Cfg {
   static constexpr int kPitch = D == 64 ? 64 : 128;        // bytes of a key's row in a stage
   static constexpr int kStage = 2 * kTile * kPitch;        // K rows, then V rows
   static constexpr int kChunks = D / 16;
+  static constexpr int kBlocks = NT == 1 ? 4 : 3;
+  static constexpr int kStages = NT == 1 ? 3 : 4;
   static constexpr size_t kSmem = static_cast<size_t>(kWarps) * kStages * kStage;
+  static_assert(kBlocks * (kSmem + 1024) <= 227 * 1024, "shared memory per SM");
 };
 
 // Byte offset of 16-byte chunk c of row r in a stage. D = 128 (and 96 in the
@@ -66,9 +87,9 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -78,6 +99,19 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// Four int8 codes (bytes e0..e3 of w) as two fp16 pairs, exactly.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &p01, uint32_t &p23) {
+  const uint32_t u = w ^ 0x80808080u;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p01) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p23) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // The dims of a head are cut into parts of 64 (and for D = 128 one of 128,
@@ -127,437 +161,514 @@ __device__ __forceinline__ void load_v_words(const uint8_t *v, int r, int g, uin
   }
 }
 
-// Partial results of a split: [sequence][kv head][row block][split] x (8 NT
-// rows x D sums, then 8 NT rows x (maximum, sum)).
-template <int D, int NT>
-constexpr int partial_floats() { return 8 * NT * (D + 2); }
+// ---------------------------------------------------------------- the cut
+// Sequence b as the cut sees it: its segments (kv heads x blocks of query
+// rows), each of kSetup + walk.count units (none without keys).
+struct SeqWork {
+  KvSeq seq;
+  int32_t prefix, segs;
+  TileWalk walk;
+  __device__ __forceinline__ uint32_t seg_units() const { return walk.count > 0 ? kSetup + walk.count : 0; }
+  __device__ __forceinline__ uint32_t units() const { return segs * seg_units(); }
+};
 
-// Block (split, kv head and row block, sequence).
+template <int ROWS>
+__device__ __forceinline__ SeqWork seq_work(const KvAttnArgs &a, int32_t b, int32_t *status) {
+  SeqWork w;
+  w.prefix = a.prefix ? __ldg(a.prefix + b) : 0;
+  w.seq = load_seq(a.s, b, a.s.max_kv, status);
+  w.segs = (w.seq.q * a.group + ROWS - 1) / ROWS * a.c.heads;
+  w.walk = tile_walk(kTile, w.prefix, w.seq.n, max(w.seq.pos0(), 0), w.seq.n, a.window);
+  return w;
+}
+
+// Units before sequence `b` and all units; called by a whole warp. (Fewer
+// than 2^31 in all: the host has checked it.)
+template <int ROWS>
+__device__ __forceinline__ void count_units(const KvAttnArgs &a, int32_t b, int32_t *status, uint32_t &before,
+                                            uint32_t &all) {
+  const int lane = threadIdx.x & 31;
+  before = all = 0;
+  for (int32_t i0 = 0; i0 < a.s.batch; i0 += 32) {
+    const int32_t i = i0 + lane;
+    const uint32_t v = i < a.s.batch ? seq_work<ROWS>(a, i, status).units() : 0;
+    if (b >= i0 && b < i0 + 32) before = all + __reduce_add_sync(0xFFFFFFFFu, i < b ? v : 0);
+    all += __reduce_add_sync(0xFFFFFFFFu, v);
+  }
+}
+
+// The sequence that unit `at` (of all) lies in, and the units before it.
+template <int ROWS>
+__device__ __forceinline__ int32_t find_unit(const KvAttnArgs &a, uint32_t at, uint32_t &before) {
+  const int lane = threadIdx.x & 31;
+  before = 0;
+  for (int32_t i0 = 0; i0 < a.s.batch; i0 += 32) {
+    const int32_t i = i0 + lane;
+    const uint32_t v = i < a.s.batch ? seq_work<ROWS>(a, i, nullptr).units() : 0;
+    uint32_t sum = v;  // inclusive scan
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += u;
+    }
+    const int32_t c = __popc(__ballot_sync(0xFFFFFFFFu, before + sum <= at));
+    if (c < 32) {
+      before += __shfl_sync(0xFFFFFFFFu, sum - v, c);
+      return i0 + c;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+  }
+  return a.s.batch;
+}
+
+// `all` units cut into pieces, at most one to a warp, whose sizes differ by at
+// most one.
+struct Cut {
+  uint32_t pieces, size, more;  // the first `more` pieces have size + 1 units
+  __device__ __forceinline__ Cut(uint32_t all, uint32_t warps) {
+    pieces = max(1u, min((all + kMinUnits - 1) / kMinUnits, warps));
+    size = all / pieces;
+    more = all - size * pieces;
+  }
+  __device__ __forceinline__ uint32_t begin(uint32_t p) const { return p * size + min(p, more); }
+  __device__ __forceinline__ uint32_t piece_of(uint32_t unit) const {
+    const uint32_t big = more * (size + 1);
+    return unit < big ? unit / (size + 1) : more + (unit - big) / size;
+  }
+};
+
+// A part of a segment in the workspace: slot 2 p of piece p where the segment
+// is the piece's first, else 2 p + 1 (it is then its last). 8 NT rows x D
+// sums, then 8 NT rows x (m, l, mv, unused).
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+constexpr int partial_floats() { return 8 * NT * (D + 4); }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
     kv_decode_kernel(const __grid_constant__ KvAttnArgs a, float *__restrict__ partial) {
-  using C = Cfg<D>;
+  using C = Cfg<D, NT>;
   constexpr int KS = D / 16;   // contraction steps of the scores
   constexpr int MT = D / 16;   // 16-dim tiles of the output
   constexpr int ROWS = 8 * NT;
+  constexpr int ST = C::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  pdl_launch_dependents();
   pdl_wait_prerequisite();
-  const int b = blockIdx.z, h = blockIdx.y % a.c.heads, rb = blockIdx.y / a.c.heads;
-  const int split = blockIdx.x, splits = gridDim.x;
-  const KvSeq seq = load_seq(a.s, b, a.s.max_kv, a.status);
-  const int rows = seq.q * a.group;  // query rows of this kv head
-  const int row0 = rb * ROWS;
-  if (row0 >= rows) return;
-  const int32_t prefix = a.prefix ? __ldg(a.prefix + b) : 0;
-  const TileWalk walk = tile_walk(kTile, prefix, seq.n, max(seq.pos0(), 0), seq.n, a.window);
-  const int per = (walk.count + splits - 1) / splits;
-  const int x0 = min(walk.count, split * per), x1 = min(walk.count, x0 + per);
-  const int32_t *table_row = a.s.table + b * a.s.table_ld;
-  uint8_t *ring = smem + warp * (kStages * C::kStage);
+  pdl_launch_dependents();  // after the wait: the join may read the lengths before its own
+  uint8_t *ring = smem + warp * (ST * C::kStage);
 
-  // this lane's query rows as the narrow operand of the scores, and as columns of S^T
-  uint32_t qf[NT][KS][2];
-  float slope[NT][2];
-  int pos[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = row0 + nt * 8 + g;
-    const bool ok = r < rows;
-    const int i = r / a.group, hq = h * a.group + (r - i * a.group);
-    const uint16_t *q = a.q.p + (seq.row0 + i) * a.q.token_stride + hq * a.q.head_stride;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      uint2 v = make_uint2(0, 0);
-      if (ok) v = __ldg(reinterpret_cast<const uint2 *>(q + k_dim<D>(t, k)));
-      qf[nt][k][0] = v.x;
-      qf[nt][k][1] = v.y;
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int rc = row0 + nt * 8 + 2 * t + e;
-      const int ic = rc / a.group;
-      pos[nt][e] = rc < rows ? seq.pos0() + ic : -1;
-      slope[nt][e] = a.slopes && rc < rows ? __ldg(a.slopes + h * a.group + (rc - ic * a.group)) * kLog2e : 0.0f;
-    }
-  }
-  // positions of the block's first and last row (no row is hidden from keys at or before pos_min within the window)
-  const int pos_min = seq.pos0() + row0 / a.group;
-  const int pos_max = seq.pos0() + (min(row0 + ROWS, rows) - 1) / a.group;
+  uint32_t all, before;
+  const uint32_t p = warp * gridDim.x + blockIdx.x;  // few pieces spread over all SMs
+  count_units<ROWS>(a, -1, p == 0 ? a.status : nullptr, before, all);
+  if (all == 0) return;
+  const Cut cut(all, gridDim.x * kWarps);
+  if (p >= cut.pieces) return;
+  uint32_t at = cut.begin(p);
+  const uint32_t begin = at, end = cut.begin(p + 1);
+  int32_t b = find_unit<ROWS>(a, at, before);
+  SeqWork work = seq_work<ROWS>(a, b, nullptr);
+
   const bool cap = a.softcap > 0.0f;
   // s = S * scale * log2(e), or with a cap c: z = S * scale / c, s = c log2(e) tanh(z)
-  const float mul = cap ? a.scale / a.softcap : a.scale * kLog2e;
+  const float score_mul = cap ? a.scale / a.softcap : a.scale * kLog2e;
   const float cap2 = a.softcap * kLog2e;
 
-  float acc[MT][NT][4];
-  float m[NT][2], l[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, l[nt][e] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.0f;
-  }
-
-  // pages and scales of the warp's next kPagesAhead tiles: lane 2 y + z holds granule z of tile y
-  int page_l = -1;
-  float ks_l = 0.0f, vs_l = 0.0f;
-  const auto fetch_pages = [&](int xw) {
-    page_l = -1;
-    ks_l = vs_l = 0.0f;
-    const int x = xw + (lane >> 1) * kWarps;
-    if (x >= x1) return;
-    const int key = walk.tile(x) * kTile + (lane & 1) * kGran;
-    if (key >= seq.n) return;
-    page_l = load_page(table_row, key >> a.c.page_shift, a.c.pages, a.status);
-    if (page_l < 0) return;
-    const int64_t at = static_cast<int64_t>(page_l) * a.c.heads + h;
-    ks_l = __ldg(a.c.ks + at);
-    vs_l = __ldg(a.c.vs + at);
-  };
-  const auto load_tile = [&](int x, int y, int stage) {  // tile x, the y-th of the fetched ones
-    const uint32_t dst = smem_addr(ring + stage * C::kStage);
-    const int key0 = walk.tile(x) * kTile;
-    int64_t base[2];
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const int p = __shfl_sync(0xFFFFFFFFu, page_l, 2 * y + z);
-      const int64_t blk = static_cast<int64_t>(p) * a.c.heads + h;
-      base[z] = p < 0 ? -1 : ((blk << a.c.page_shift) + ((key0 + z * kGran) & (a.c.page - 1))) * D;
+  while (at < end) {
+    while (at >= before + work.units()) {  // on to the next sequence that has keys
+      before += work.units();
+      work = seq_work<ROWS>(a, ++b, nullptr);
     }
+    const KvSeq seq = work.seq;
+    const TileWalk walk = work.walk;
+    const int32_t prefix = work.prefix;
+    const uint32_t seg_units = work.seg_units();
+    const int32_t seg = static_cast<int32_t>((at - before) / seg_units);
+    const uint32_t seg0 = before + seg * seg_units, seg_end = min(seg0 + seg_units, end);
+    // tiles of the part: units from kSetup on
+    const int x0 = max(static_cast<int>(at - seg0) - kSetup, 0), x1 = static_cast<int>(seg_end - seg0) - kSetup;
+    const bool first = begin >= seg0;
+    at = seg_end;
+    if (x1 <= x0) continue;
+    const int rbs = work.segs / a.c.heads, h = seg / rbs;  // the row blocks of a head side by side: its keys stay in L2
+    const int rows = seq.q * a.group, row0 = (seg - h * rbs) * ROWS;
+    const int32_t *table_row = a.s.table + b * a.s.table_ld;
+
+    // this lane's query rows as the narrow operand of the scores (scaled into fp16's range), and as columns of S^T
+    uint32_t qf[NT][KS][2];
+    float slope[NT][2], mul[NT][2];
+    int pos[NT][2];
 #pragma unroll
-    for (int i = 0; i < C::kChunks; ++i) {
-      const int idx = i * 32 + lane, r = idx / C::kChunks, c = idx % C::kChunks;
-      const int64_t bz = r >= kGran ? base[1] : base[0];
-      if (bz >= 0) {
-        const int64_t src = bz + (r & (kGran - 1)) * D + 16 * c;
-        cp_async16(dst + stage_off<D>(r, c), a.c.k + src);
-        cp_async16(dst + kTile * C::kPitch + stage_off<D>(r, c), a.c.v + src);
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + g;
+      const bool ok = r < rows;
+      const int i = r / a.group, hq = h * a.group + (r - i * a.group);
+      const uint16_t *q = a.q.p + (seq.row0 + i) * a.q.token_stride + hq * a.q.head_stride;
+      uint32_t big = 0;  // bits of the row's largest magnitude
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint2 v = make_uint2(0, 0);
+        if (ok) v = __ldg(reinterpret_cast<const uint2 *>(q + k_dim<D>(t, k)));
+        qf[nt][k][0] = v.x;
+        qf[nt][k][1] = v.y;
+        big = max(big, max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu)));
+      }
+      big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+      big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+      // 2^(14 - exponent of the largest), both ways; a zero row stays as it is
+      const int ex = min(max(static_cast<int>(big >> 7), 16), 254);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 127 + 14 - ex > 254 ? 254 : 127 + 127 + 14 - ex) << 23);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+          qf[nt][k][z] = pack_f16x2(bf16_lo(qf[nt][k][z]) * up, bf16_hi(qf[nt][k][z]) * up);
+      const float down = 1.0f / up;  // exact
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mul[nt][e] = __shfl_sync(0xFFFFFFFFu, down, 4 * (2 * t + e)) * score_mul;
+        const int rc = row0 + nt * 8 + 2 * t + e;
+        const int ic = rc / a.group;
+        pos[nt][e] = rc < rows ? seq.pos0() + ic : -1;
+        slope[nt][e] = a.slopes && rc < rows ? __ldg(a.slopes + h * a.group + (rc - ic * a.group)) * kLog2e : 0.0f;
       }
     }
-  };
+    // positions of the first and last row (no row is hidden from keys at or before pos_min within the window)
+    const int pos_min = seq.pos0() + row0 / a.group;
+    const int pos_max = seq.pos0() + (min(row0 + ROWS, rows) - 1) / a.group;
 
-  // The warp's tiles are x0 + warp, x0 + warp + kWarps, ... The pages of tile
-  // number y (from 0) are fetched kPagesAhead at a time; loads run kStages - 1
-  // tiles ahead, so the fetched window is refilled when its last tile is
-  // loaded, and the scales of a loaded tile travel with it in registers.
-  float ksc[kStages][2], vsc[kStages][2];
-  int pgc[kStages][2];
-  int y_load = 0;  // next tile to load, as a count of this warp's tiles
-  const int ny = x1 - x0 > warp ? (x1 - x0 - warp + kWarps - 1) / kWarps : 0;
-  const auto stage_tile = [&](int slot) {
-    if (y_load < ny) {
-      const int y = y_load % kPagesAhead;
-      if (y == 0) fetch_pages(x0 + warp + y_load * kWarps);
-      load_tile(x0 + warp + y_load * kWarps, y, slot);
+    float acc[MT][NT][4];
+    float m[NT][2], l[NT][2], mv[NT][2];
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        pgc[slot][z] = __shfl_sync(0xFFFFFFFFu, page_l, 2 * y + z);
-        ksc[slot][z] = __shfl_sync(0xFFFFFFFFu, ks_l, 2 * y + z);
-        vsc[slot][z] = __shfl_sync(0xFFFFFFFFu, vs_l, 2 * y + z);
-      }
-      ++y_load;
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[nt][e] = mv[nt][e] = -INFINITY, l[nt][e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.0f;
     }
-    cp_async_commit();
-  };
 
-  const auto compute_tile = [&](int x, int slot) {
-    const uint8_t *ks = ring + slot * C::kStage, *vs = ks + kTile * C::kPitch;
-    const int key0 = walk.tile(x) * kTile;
-    float s[2][NT][4];
+    // Page, k's scale and log2 of v's scale of 32 tiles, one to a lane: of the
+    // window that is being computed and, fetched when it begins, of the next.
+    int page_c, page_n;
+    float ks_c, vs_c, ks_n, vs_n;
+    const auto fetch = [&](int x) {  // tiles x .. x + 31
+      page_n = -1;
+      ks_n = 0.0f;
+      vs_n = -INFINITY;
+      if (x + lane >= x1) return;
+      page_n = load_page(table_row, walk.tile(x + lane) * kTile >> a.c.page_shift, a.c.pages, a.status);
+      if (page_n < 0) return;
+      const int64_t i = static_cast<int64_t>(page_n) * a.c.heads + h;
+      ks_n = __ldg(a.c.ks + i);
+      vs_n = log2f(__ldg(a.c.vs + i));
+    };
+    const auto load_tile = [&](int x, int win, int slot) {  // win: first tile of the window being computed
+      if (x < x1) {
+        const int page = x < win + 32 ? __shfl_sync(0xFFFFFFFFu, page_c, x - win) : __shfl_sync(0xFFFFFFFFu, page_n, x - win - 32);
+        if (page >= 0) {
+          const uint32_t dst = smem_addr(ring + slot * C::kStage);
+          const int in_page = (walk.tile(x) * kTile) & (a.c.page - 1);
+          const int64_t src = (((static_cast<int64_t>(page) * a.c.heads + h) << a.c.page_shift) + in_page) * D + 16 * lane;
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      uint32_t w0[KS], w1[KS];
-      load_k_words<D>(ks, mt * kGran + g, t, w0);
-      load_k_words<D>(ks, mt * kGran + g + 8, t, w1);
+          for (int i = 0; i < C::kChunks / 2; ++i) {  // the tile's rows are one run of kTile * D bytes
+            const int idx = i * 32 + lane, r = idx / C::kChunks, c = idx % C::kChunks;
+            cp_async16(dst + stage_off<D>(r, c), a.c.k + src + 512 * i);
+            cp_async16(dst + kTile * C::kPitch + stage_off<D>(r, c), a.c.v + src + 512 * i);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+
+    const auto compute_tile = [&](int x, int slot, int page, float k_scale, float v_log) {
+      const uint8_t *ks = ring + slot * C::kStage, *vs = ks + kTile * C::kPitch;
+      const int key0 = walk.tile(x) * kTile;
+      float s[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+      {
+        uint32_t w0[KS], w1[KS];
+        load_k_words<D>(ks, g, t, w0);
+        load_k_words<D>(ks, g + 8, t, w1);
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint32_t a0, a1, a2, a3;
-        codes_to_bf16(w0[k], a0, a2);
-        codes_to_bf16(w1[k], a1, a3);
+        for (int k = 0; k < KS; ++k) {
+          uint32_t a0, a1, a2, a3;
+          codes_to_f16(w0[k], a0, a2);
+          codes_to_f16(w1[k], a1, a3);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(s[mt][nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
-      }
-    }
-    // scores, in units of log2; element e of s[mt][nt]: key mt * 16 + g + 8 (e >> 1), row 2 t + (e & 1)
-    const bool whole = key0 + kTile - 1 <= pos_min && (a.window == 0 || key0 > pos_max - a.window) &&
-                       pgc[slot][0] >= 0 && pgc[slot][1] >= 0;
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const float f = ksc[slot][mt] * mul;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = s[mt][nt][e] * f;
-          if (cap) v = cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(v * (2.0f * kLog2e)));
-          s[mt][nt][e] = v;
+          for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
         }
       }
-    }
-    if (a.slopes || !whole) {
+      // scores, in units of log2; element e of s[nt]: key g + 8 (e >> 1), row 2 t + (e & 1)
+      const bool whole = key0 + kTile - 1 <= pos_min && (a.window == 0 || key0 > pos_max - a.window) && page >= 0;
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] *= k_scale * mul[nt][e & 1];
+      if (cap) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[nt][e] = cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(s[nt][e] * (2.0f * kLog2e)));
+      }
+      if (a.slopes || !whole) {
+        bool any = whole;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int j = key0 + mt * kGran + g + 8 * (e >> 1), p = pos[nt][e & 1];
-            float v = s[mt][nt][e] + slope[nt][e & 1] * static_cast<float>(j - p);
+            const int j = key0 + g + 8 * (e >> 1), at_q = pos[nt][e & 1];
+            float v = s[nt][e] + slope[nt][e & 1] * static_cast<float>(j - at_q);
             if (!whole) {
-              const bool seen = pgc[slot][mt] >= 0 && j < seq.n && p >= 0 &&
-                                ((j <= p && (a.window == 0 || p - j < a.window)) || j < prefix);
+              const bool seen = page >= 0 && j < seq.n && at_q >= 0 &&
+                                ((j <= at_q && (a.window == 0 || at_q - j < a.window)) || j < prefix);
               v = seen ? v : -INFINITY;
+              any = any || seen;
             }
-            s[mt][nt][e] = v;
+            s[nt][e] = v;
           }
-    }
-    bool grew = false;
-    float al[NT][2];
+        // a page of which no row sees anything may hold anything: it adds nothing
+        if (!__any_sync(0xFFFFFFFFu, any)) return;
+      }
+      bool grew = false;
+      float al[NT][2], fv[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float v = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+        for (int e = 0; e < 2; ++e) {
+          float v = fmaxf(s[nt][e], s[nt][e + 2]);
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-        al[nt][e] = 1.0f;
-        if (v > m[nt][e]) {
-          al[nt][e] = ex2(m[nt][e] - v);
-          m[nt][e] = v;
-          grew = true;
+          for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+          al[nt][e] = 1.0f;
+          if (v > m[nt][e]) {
+            l[nt][e] *= ex2(m[nt][e] - v);
+            m[nt][e] = v;
+          }
+          if (v + v_log > mv[nt][e]) {
+            al[nt][e] = ex2(mv[nt][e] - (v + v_log));
+            mv[nt][e] = v + v_log;
+            grew = true;
+          }
+          // from 2^(s - m) to w (its exponent held in range: it is large only
+          // where 2^(s - m) is 0); 0 for a row that sees nothing of the page
+          const float x = m[nt][e] + v_log - mv[nt][e];
+          fv[nt][e] = v == -INFINITY || mv[nt][e] == -INFINITY ? 0.0f : ex2(x > 126.0f ? 126.0f : x);
         }
+      if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][nt][e] *= al[nt][e & 1];
       }
-    if (__any_sync(0xFFFFFFFFu, grew)) {
+      uint32_t ph[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        l[nt][0] *= al[nt][0];
-        l[nt][1] *= al[nt][1];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][nt][e] *= al[nt][e & 1];
-      }
-    }
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
+        float w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float ref = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];  // a row that has seen no key yet
-          p[e] = ex2(s[mt][nt][e] - ref);
-          l[nt][e & 1] += p[e];
-          // (not 0 times the scale of a page that no row sees, which may be anything)
-          p[e] = whole || s[mt][nt][e] != -INFINITY ? p[e] * vsc[slot][mt] : 0.0f;
+          w[e] = ex2(s[nt][e] - ref);
+          l[nt][e & 1] += w[e];
+          w[e] *= fv[nt][e & 1];
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t hi = pack_bf16x2(p[2 * k], p[2 * k + 1]);
-          const uint32_t lo = pack_bf16x2(p[2 * k] - bf16_lo(hi), p[2 * k + 1] - bf16_hi(hi));
-          ph[nt][k] = transpose8x8(hi);
-          pl[nt][k] = transpose8x8(lo);
-        }
+        ph[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+        ph[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
       }
       uint32_t v0[D / 32], v1[D / 32], v2[D / 32], v3[D / 32];
-      load_v_words<D>(vs, mt * kGran + 2 * t, g, v0);
-      load_v_words<D>(vs, mt * kGran + 2 * t + 1, g, v1);
-      load_v_words<D>(vs, mt * kGran + 2 * t + 8, g, v2);
-      load_v_words<D>(vs, mt * kGran + 2 * t + 9, g, v3);
+      load_v_words<D>(vs, 2 * t, g, v0);
+      load_v_words<D>(vs, 2 * t + 1, g, v1);
+      load_v_words<D>(vs, 2 * t + 8, g, v2);
+      load_v_words<D>(vs, 2 * t + 9, g, v3);
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const uint32_t sel = half ? 0x7362u : 0x5140u;
           uint32_t a0, a1, a2, a3;
-          codes_to_bf16(__byte_perm(v0[w], v1[w], sel), a0, a1);
-          codes_to_bf16(__byte_perm(v2[w], v3[w], sel), a2, a3);
+          codes_to_f16(__byte_perm(v0[w], v1[w], sel), a0, a1);
+          codes_to_f16(__byte_perm(v2[w], v3[w], sel), a2, a3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_bf16_16816(acc[2 * w + half][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-            mma_bf16_16816(acc[2 * w + half][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
-          }
+          for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[2 * w + half][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
         }
       }
-    }
-  };
+    };
 
+    fetch(x0);
+    page_c = page_n, ks_c = ks_n, vs_c = vs_n;
+    fetch(x0 + 32);
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) stage_tile(i);
-  for (int y = 0; y < ny; y += kStages) {
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) {
-      if (y + i < ny) {
-        cp_async_wait<kStages - 2>();
-        __syncwarp();  // every lane's copies of this tile have landed, and all have read the slot loaded next
-        stage_tile((i + kStages - 1) % kStages);
-        compute_tile(x0 + warp + (y + i) * kWarps, i);
+    for (int i = 0; i < ST - 1; ++i) load_tile(x0 + i, x0, i);
+    int win = x0, slot = 0;
+#pragma unroll 1
+    for (int x = x0; x < x1; ++x) {
+      if (x == win + 32) {
+        win = x;
+        page_c = page_n, ks_c = ks_n, vs_c = vs_n;
+        fetch(x + 32);
       }
+      cp_async_wait<ST - 2>();
+      __syncwarp();  // every lane's copies of this tile have landed, and all have read the slot loaded next
+      load_tile(x + ST - 1, win, slot == 0 ? ST - 1 : slot - 1);
+      compute_tile(x, slot, __shfl_sync(0xFFFFFFFFu, page_c, x - win), __shfl_sync(0xFFFFFFFFu, ks_c, x - win),
+                   __shfl_sync(0xFFFFFFFFu, vs_c, x - win));
+      slot = slot + 1 == ST ? 0 : slot + 1;
     }
-  }
-  cp_async_wait<0>();
-  __syncthreads();
+    cp_async_wait<0>();
+    __syncwarp();
 
-  // join the warps: sums of each row in shared memory, scaled to the row's maximum
-  float *s_acc = reinterpret_cast<float *>(smem);               // [warp][row][D]
-  float *s_ml = s_acc + kWarps * ROWS * D;                      // [warp][row](maximum, sum)
+    const bool mine = x0 == 0 && x1 == walk.count;
+    float *out_p = partial + static_cast<int64_t>(2 * p + (first ? 0 : 1)) * partial_floats<D, NT>();
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float v = l[nt][e];
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[nt][e];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-      const int r = nt * 8 + 2 * t + e;
-      if (g == 0) {
-        s_ml[(warp * ROWS + r) * 2] = m[nt][e];
-        s_ml[(warp * ROWS + r) * 2 + 1] = v;
+        for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const int r = nt * 8 + 2 * t + e;
+        if (row0 + r >= rows) continue;
+        if (mine) {
+          const float inv = sum > 0.0f && mv[nt][e] != -INFINITY ? ex2(mv[nt][e] - m[nt][e]) / sum : 0.0f;
+          const int qi = (row0 + r) / a.group, hq = h * a.group + (row0 + r - qi * a.group);
+          const int64_t elem = (static_cast<int64_t>(seq.row0 + qi) * a.q_heads + hq) * D;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) store_out2(a, elem + v_dim<D>(g, i), acc[i][nt][e] * inv, acc[i][nt][e + 2] * inv);
+        } else {
+          if (g == 0) *reinterpret_cast<float4 *>(out_p + ROWS * D + 4 * r) = make_float4(m[nt][e], sum, mv[nt][e], 0.0f);
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            *reinterpret_cast<float2 *>(out_p + r * D + v_dim<D>(g, i)) = make_float2(acc[i][nt][e], acc[i][nt][e + 2]);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        *reinterpret_cast<float2 *>(s_acc + (warp * ROWS + r) * D + v_dim<D>(g, i)) =
-            make_float2(acc[i][nt][e], acc[i][nt][e + 2]);
-    }
-  __syncthreads();
-  const int row_blocks = gridDim.y / a.c.heads;
-  float *out_p = partial +
-                 (((static_cast<int64_t>(b) * a.c.heads + h) * row_blocks + rb) * splits + split) * partial_floats<D, NT>();
-  for (int i = threadIdx.x; i < ROWS * (D / 4); i += kThreads) {
-    const int r = i / (D / 4), d = 4 * (i % (D / 4));
-    if (row0 + r >= rows) continue;
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[(w * ROWS + r) * 2]);
-    float ll = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (mm != -INFINITY) {
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(s_ml[(w * ROWS + r) * 2] - mm);
-        ll += f * s_ml[(w * ROWS + r) * 2 + 1];
-        const float4 v = *reinterpret_cast<const float4 *>(s_acc + (w * ROWS + r) * D + d);
-        y[0] += f * v.x, y[1] += f * v.y, y[2] += f * v.z, y[3] += f * v.w;
-      }
-    }
-    if (splits == 1) {
-      const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] *= inv;
-      const int qi = (row0 + r) / a.group, hq = h * a.group + (row0 + r - qi * a.group);
-      store_out4(a, (static_cast<int64_t>(seq.row0 + qi) * a.q_heads + hq) * D + d, y);
-    } else {
-      *reinterpret_cast<float4 *>(out_p + r * D + d) = make_float4(y[0], y[1], y[2], y[3]);
-      if (d == 0) *reinterpret_cast<float2 *>(out_p + ROWS * D + 2 * r) = make_float2(mm, ll);
-    }
   }
 }
 
-// Joins the splits: one warp per (row of a kv head, sequence).
+// Joins the parts of each segment row; block (kv head and row, sequence). A
+// segment that one piece holds is written already; one without keys is zeros.
 template <int D, int NT>
-__global__ void __launch_bounds__(128) kv_join_kernel(const __grid_constant__ KvAttnArgs a,
-                                                      const float *__restrict__ partial, int splits, int row_blocks) {
-  constexpr int ROWS = 8 * NT;
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_constant__ KvAttnArgs a,
+                                                                  const float *__restrict__ partial, uint32_t warps,
+                                                                  int max_rows) {
+  constexpr int ROWS = 8 * NT, F = partial_floats<D, NT>();
+  __shared__ float s_acc[kJoinWarps][D];
+  __shared__ float s_ml[kJoinWarps][3];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.y;
+  const int h = blockIdx.x / max_rows, row = blockIdx.x % max_rows;
+  // the lengths: written before the kernel that this one follows passed its own wait
+  uint32_t before, all;
+  count_units<ROWS>(a, b, nullptr, before, all);
+  const SeqWork work = seq_work<ROWS>(a, b, nullptr);
+  const Cut cut(all, warps);
+  const int rbs = work.segs / a.c.heads;
+  const uint32_t s0 = before + (h * rbs + row / ROWS) * work.seg_units();
+  uint32_t p0 = 0, p1 = 0;
+  if (row < work.seq.q * a.group && work.walk.count > 0) {
+    p0 = cut.piece_of(s0 + kSetup);
+    p1 = cut.piece_of(s0 + work.seg_units() - 1);
+  }
   pdl_launch_dependents();
   pdl_wait_prerequisite();
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.y;
-  const KvSeq seq = load_seq(a.s, b, a.s.max_kv, nullptr);
-  const int64_t id = blockIdx.x * 4 + (threadIdx.x >> 5);  // kv head, row
-  const int h = static_cast<int>(id / (row_blocks * ROWS)), row = static_cast<int>(id % (row_blocks * ROWS));
-  if (h >= a.c.heads || row >= seq.q * a.group) return;
-  const int rb = row / ROWS, r = row % ROWS;
-  const float *p = partial + ((static_cast<int64_t>(b) * a.c.heads + h) * row_blocks + rb) * splits * partial_floats<D, NT>();
-  float mm = -INFINITY;
-  for (int s = 0; s < splits; ++s) mm = fmaxf(mm, p[s * partial_floats<D, NT>() + ROWS * D + 2 * r]);
-  float ll = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (mm != -INFINITY) {
-    for (int s = 0; s < splits; ++s) {
-      const float *ps = p + s * partial_floats<D, NT>();
-      const float2 ml = *reinterpret_cast<const float2 *>(ps + ROWS * D + 2 * r);
-      const float f = ex2(ml.x - mm);
-      ll += f * ml.y;
-      if (4 * lane < D) {
-        const float4 v = *reinterpret_cast<const float4 *>(ps + r * D + 4 * lane);
-        y[0] += f * v.x, y[1] += f * v.y, y[2] += f * v.z, y[3] += f * v.w;
-      }
+  if (row >= work.seq.q * a.group || (work.walk.count > 0 && p0 == p1)) return;
+  float mm = -INFINITY, mv = -INFINITY, ll = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const auto add = [&](float m1, float l1, float mv1, float4 v) {
+    const float m2 = fmaxf(mm, m1), mv2 = fmaxf(mv, mv1);
+    if (m2 != -INFINITY) ll = ll * ex2(mm - m2) + l1 * ex2(m1 - m2);
+    if (mv2 != -INFINITY) {
+      const float f0 = ex2(mv - mv2), f1 = ex2(mv1 - mv2);
+      y[0] = y[0] * f0 + v.x * f1, y[1] = y[1] * f0 + v.y * f1, y[2] = y[2] * f0 + v.z * f1, y[3] = y[3] * f0 + v.w * f1;
     }
+    mm = m2;
+    mv = mv2;
+  };
+  if (work.walk.count > 0) {
+    const int r = row % ROWS;
+    for (uint32_t p = p0 + warp; p <= p1; p += kJoinWarps) {
+      const float *part = partial + static_cast<int64_t>(2 * p + (cut.begin(p) < s0 ? 1 : 0)) * F;
+      const float4 ml = *reinterpret_cast<const float4 *>(part + ROWS * D + 4 * r);
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (4 * lane < D) v = *reinterpret_cast<const float4 *>(part + r * D + 4 * lane);
+      add(ml.x, ml.y, ml.z, v);
+    }
+    if (4 * lane < D) *reinterpret_cast<float4 *>(&s_acc[warp][4 * lane]) = make_float4(y[0], y[1], y[2], y[3]);
+    if (lane == 0) s_ml[warp][0] = mm, s_ml[warp][1] = ll, s_ml[warp][2] = mv;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (4 * lane < D) v = *reinterpret_cast<const float4 *>(&s_acc[w][4 * lane]);
+      add(s_ml[w][0], s_ml[w][1], s_ml[w][2], v);
+    }
+  } else if (warp > 0) {
+    return;
   }
   if (4 * lane >= D) return;
-  const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+  const float inv = ll > 0.0f && mv != -INFINITY ? ex2(mv - mm) / ll : 0.0f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] *= inv;
   const int qi = row / a.group, hq = h * a.group + (row - qi * a.group);
-  store_out4(a, (static_cast<int64_t>(seq.row0 + qi) * a.q_heads + hq) * D + 4 * lane, y);
+  store_out4(a, (static_cast<int64_t>(work.seq.row0 + qi) * a.q_heads + hq) * D + 4 * lane, y);
 }
 
-struct DecodePlan {
-  int nt, row_blocks, splits;
-  size_t bytes;
-};
-
-DecodePlan decode_plan(const KvAttnArgs &a, int num_sms) {
-  DecodePlan p;
-  const int64_t rows = static_cast<int64_t>(a.s.max_q) * a.group;
-  p.nt = rows <= 8 ? 1 : 2;
-  p.row_blocks = static_cast<int>((rows + 8 * p.nt - 1) / (8 * p.nt));
-  const int64_t blocks = static_cast<int64_t>(a.s.batch) * a.c.heads * p.row_blocks;
-  const int64_t most = (a.s.max_kv + kTile * kWarps - 1) / (kTile * kWarps);  // a tile for each warp of a split
-  int64_t want = (num_sms + blocks - 1) / blocks;
-  if (want > most) want = most;
-  p.splits = static_cast<int>(want < 1 ? 1 : want);
-  p.bytes = p.splits == 1 ? 0 : static_cast<size_t>(blocks) * p.splits * 8 * p.nt * (a.c.d + 2) * sizeof(float);
-  return p;
-}
+bool wide_rows(const KvAttnArgs &a) { return static_cast<int64_t>(a.s.max_q) * a.group > 8; }
 
 template <int D, int NT>
-cudaError_t launch_t(const KvAttnArgs &a, const DecodePlan &p, float *partial, cudaStream_t s) {
-  constexpr size_t kJoin = static_cast<size_t>(kWarps) * 8 * NT * (D + 2) * sizeof(float);
-  constexpr size_t kSmem = Cfg<D>::kSmem > kJoin ? Cfg<D>::kSmem : kJoin;
-  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-  cudaError_t e = ensure_kernel_smem<kv_decode_kernel<D, NT>>(static_cast<int>(kSmem), true);
+cudaError_t launch_t(const KvAttnArgs &a, float *partial, int num_sms, cudaStream_t s) {
+  using C = Cfg<D, NT>;
+  cudaError_t e = ensure_kernel_smem<kv_decode_kernel<D, NT>>(static_cast<int>(C::kSmem), true);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.splits, a.c.heads * p.row_blocks, a.s.batch);
+  cfg.gridDim = dim3(num_sms * C::kBlocks);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const uint32_t warps = cfg.gridDim.x * kWarps;
   e = cudaLaunchKernelEx(&cfg, kv_decode_kernel<D, NT>, a, partial);
-  if (e != cudaSuccess || p.splits == 1) return e;
-  cfg.gridDim = dim3((a.c.heads * p.row_blocks * 8 * NT + 3) / 4, a.s.batch);
-  cfg.blockDim = dim3(128);
+  if (e != cudaSuccess) return e;
+  const int max_rows = a.s.max_q * a.group;
+  cfg.gridDim = dim3(a.c.heads * max_rows, a.s.batch);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT>, a, static_cast<const float *>(partial), p.splits, p.row_blocks);
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT>, a, static_cast<const float *>(partial), warps, max_rows);
 }
 
 template <int D>
-cudaError_t launch_d(const KvAttnArgs &a, const DecodePlan &p, float *partial, cudaStream_t s) {
-  return p.nt == 1 ? launch_t<D, 1>(a, p, partial, s) : launch_t<D, 2>(a, p, partial, s);
+cudaError_t launch_d(const KvAttnArgs &a, float *partial, int num_sms, cudaStream_t s) {
+  return wide_rows(a) ? launch_t<D, 2>(a, partial, num_sms, s) : launch_t<D, 1>(a, partial, num_sms, s);
 }
 
 }  // namespace
 
-size_t kv_decode_workspace_bytes(const KvAttnArgs &a, int num_sms) { return decode_plan(a, num_sms).bytes; }
+bool kv_decode_fits(const KvAttnArgs &a) {  // all units in 31 bits
+  const int64_t rows = static_cast<int64_t>(a.s.max_q) * a.group;
+  const int64_t segs = (rows + 7) / 8 * a.c.heads, per = a.s.max_kv / kTile + 2 + kSetup;
+  return segs * a.s.batch <= INT32_MAX / per;
+}
+
+size_t kv_decode_workspace_bytes(const KvAttnArgs &a, int num_sms) {
+  // two parts a warp
+  const int64_t nt = wide_rows(a) ? 2 : 1, warps = static_cast<int64_t>(num_sms) * (nt == 2 ? 3 : 4) * kWarps;
+  return static_cast<size_t>(2 * warps * 8 * nt * (a.c.d + 4)) * sizeof(float);
+}
 
 cudaError_t launch_kv_decode(const KvAttnArgs &a, void *workspace, int num_sms, cudaStream_t s) {
-  const DecodePlan p = decode_plan(a, num_sms);
   float *partial = static_cast<float *>(workspace);
   switch (a.c.d) {
-    case 64: return launch_d<64>(a, p, partial, s);
-    case 96: return launch_d<96>(a, p, partial, s);
-    case 128: return launch_d<128>(a, p, partial, s);
+    case 64: return launch_d<64>(a, partial, num_sms, s);
+    case 96: return launch_d<96>(a, partial, num_sms, s);
+    case 128: return launch_d<128>(a, partial, num_sms, s);
     default: return cudaErrorInvalidValue;
   }
 }

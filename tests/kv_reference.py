@@ -172,7 +172,7 @@ def gather(cache: Cache, table, first, start, keep):
     return outs
 
 
-def attention(cache: Cache, s: Seqs, q, scale, softcap=0.0, window=0, slopes=None, prefix=None, weight_err=2.0 ** -16):
+def attention(cache: Cache, s: Seqs, q, scale, softcap=0.0, window=0, slopes=None, prefix=None, few=True):
     """(out, tolerance) float64 [tokens, q_heads, d], NaN in rows of no sequence.
 
     The tolerance counts what fp32 arithmetic may add, to first order. With
@@ -181,8 +181,10 @@ def attention(cache: Cache, s: Seqs, q, scale, softcap=0.0, window=0, slopes=Non
       (times its factor), and its few further operations by 8 u of the
       largest value that enters them: delta;
       a weight is exp(score): off by a factor 1 + 2 delta against the row's
-      maximum, by 2^-21 in the exponential and by `weight_err` where it is
-      rounded to bf16 for the second product;
+      maximum, by 2^-21 in the exponential and, where it is rounded for the
+      second product, by 2^-11 with `few` query rows of a kv head (fp16, and
+      there by at least 2^-25 of the row's largest weight times scale, which
+      meets a code of at most 127), else by 2^-8 (bf16);
       sums of n terms in fp32 by n u; the quotient by 2 u more.
     All of that times sum_j p_j |v_j| / sum_j p_j, then one rounding to bf16
     (2^-8 of the value). A relative bound ends where numbers do: against the
@@ -190,6 +192,7 @@ def attention(cache: Cache, s: Seqs, q, scale, softcap=0.0, window=0, slopes=Non
     below 2^-126 may become 0 and so may its product with v's scale, which
     moves the sum over v by at most 2^-126 |v_j| and 2^-126 |code_j|."""
     u = 2.0 ** -23
+    weight_err = 2.0 ** -11 if few else 2.0 ** -8
     tokens, hq, d = q.shape
     heads = cache.k.shape[1]
     g = hq // heads
@@ -230,6 +233,10 @@ def attention(cache: Cache, s: Seqs, q, scale, softcap=0.0, window=0, slopes=Non
             dmax = np.where(seen, delta, 0.0).max(-1, keepdims=True, initial=0.0)
             rel = 2 * dmax + 8 * u * np.abs(np.where(np.isinf(top), 0.0, top)) + 2.0 ** -21 + weight_err + (n + 4) * u
             e = p @ np.abs(vh) / safe * rel
+            if few:
+                page = s.table[b, np.arange(n) // cache.page].astype(np.int64)
+                largest = (p * cache.vs[page, h // g].astype(np.float64)).max(-1, keepdims=True, initial=0.0)
+                e = e + 2.0 ** -25 * 127 * seen.sum(-1, keepdims=True) * largest / safe
             e = e + 2.0 ** -126 * (np.abs(vh).sum(0) + 127 * n)
             tol[rows, h] = e + 2.0 ** -8 * (np.abs(out[rows, h]) + e)
     return out, tol

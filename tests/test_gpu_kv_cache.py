@@ -165,13 +165,12 @@ def test_gather(d, page, heads, dtype):
 
 
 # ------------------------------------------------------------------ attention
-def check_attention(rng, s, cache, hq, weight_err=None, cacheable=None, **kw):
+def check_attention(rng, s, cache, hq, **kw):
     d, heads = cache.d, cache.k.shape[1]
     q = bf16_rows(rng, s.tokens, hq, d)
     scale = kw.pop("scale", d ** -0.5)
-    if weight_err is None:
-        weight_err = 2.0 ** -16 if int(s.new.max()) * (hq // heads) <= 32 else 2.0 ** -8
-    want, tol = R.attention(cache, s, synth.bits_to_f32(q), np.float32(scale), weight_err=weight_err,
+    few = int(s.new.max()) * (hq // heads) <= 32
+    want, tol = R.attention(cache, s, synth.bits_to_f32(q), np.float32(scale), few=few,
                             slopes=kw.get("slopes"), prefix=kw.get("prefix"), softcap=kw.get("softcap", 0.0),
                             window=kw.get("window", 0))
     keep = bf16_rows(rng, s.tokens, hq, d)
@@ -179,8 +178,7 @@ def check_attention(rng, s, cache, hq, weight_err=None, cacheable=None, **kw):
     args = dict(scale=scale, softcap=kw.get("softcap", 0.0), window=kw.get("window", 0),
                 slopes=None if kw.get("slopes") is None else dev(kw["slopes"]),
                 prefix_len=None if kw.get("prefix") is None else dev(kw["prefix"]))
-    c = to_dev(cache) if cacheable is None else cacheable
-    W.w8a8_kv_attention(dev_bf16(q), c, batch_of(s), out=out, **args)
+    W.w8a8_kv_attention(dev_bf16(q), to_dev(cache), batch_of(s), out=out, **args)
     got_bits = host_bf16(out)
     got = synth.bits_to_f32(got_bits).astype(np.float64)
     nobody = np.isnan(want)
@@ -416,7 +414,7 @@ def test_layer_chain_from_projection_to_output_projection():
         assert_cache(c, cache)
         few = int(s.new.max()) * (hq // hkv) <= 32
         want, tol = R.attention(cache, s, synth.bits_to_f32(host_bf16(q)), np.float32(d ** -0.5),
-                                weight_err=2.0 ** -16 if few else 2.0 ** -8)
+                                few=few)
         return q, want, tol
 
     x = dev_bf16(synth.activations(rng, s.tokens, hid))
@@ -490,7 +488,7 @@ def test_offsets_past_32_bits():
         q = bf16_rows(rng, s.tokens, hq, d)
         out = W.w8a8_kv_attention(dev_bf16(q), c, batch_of(s))
         few = max(new) <= 32
-        want, tol = R.attention(small, s_low, synth.bits_to_f32(q), np.float32(d ** -0.5), weight_err=2.0 ** -16 if few else 2.0 ** -8)
+        want, tol = R.attention(small, s_low, synth.bits_to_f32(q), np.float32(d ** -0.5), few=few)
         assert (np.abs(synth.bits_to_f32(host_bf16(out)) - want) <= tol).all()
         ko, vo = W.w8a8_kv_gather(c, dev(table), dev(np.zeros(2, np.int32)),
                                   dev(np.concatenate([[0], np.cumsum(s.kv)]).astype(np.int32)), rows=int(s.kv.sum()),
