@@ -440,10 +440,11 @@ size_t int8_mixed_decomp_gemm_tc_workspace_size(int64_t M, int64_t N, int32_t ca
  *
  * The lengths and the page table are read on the device, so one captured
  * graph serves growing sequences. What the host cannot check is checked
- * there: a sequence whose seq_start descends or passes the call's row count,
- * that has more than max_q_len new tokens, or whose kv_len is negative or
- * past max_kv_len is skipped (its outputs keep what they held) and sets
- * W8A8_ERR_BAD_SEQUENCE in the device status word; a page table entry outside
+ * there: a sequence whose rows pass the call's row count, that has more than
+ * max_q_len new tokens, or whose kv_len is negative or past max_kv_len is
+ * skipped (its outputs keep what they held) and sets W8A8_ERR_BAD_SEQUENCE in
+ * the device status word (so does a seq_start that descends, after which it
+ * is left open which sequences are served); a page table entry outside
  * [0, num_pages) that is needed sets W8A8_ERR_BAD_PAGE, is not dereferenced,
  * and its tokens are neither stored nor seen (read back as 0). Entries past
  * a sequence's last page are not read.
@@ -519,9 +520,9 @@ w8a8_status w8a8_kv_append(const w8a8_kv_cache *cache, const w8a8_kv_batch *batc
  *   k_out, v_out  device [rows, kv_heads, head_dim] dense, 16-byte aligned;
  *               one of them may be NULL. Rows at and past row_start[batch]
  *               keep what they held.
- * A sequence whose row_start descends or passes `rows`, or whose positions
- * are not all in [0, max_pages * page_size), is skipped
- * (W8A8_ERR_BAD_SEQUENCE).
+ * A sequence whose rows pass `rows`, or whose positions are not all in
+ * [0, max_pages * page_size), is skipped (W8A8_ERR_BAD_SEQUENCE, which a
+ * descending row_start also sets).
  */
 w8a8_status w8a8_kv_gather(const w8a8_kv_cache *cache, const int32_t *page_table, int64_t page_table_ld, int32_t batch,
                            int32_t max_pages, const int32_t *first_pos, const int32_t *row_start, int64_t rows,

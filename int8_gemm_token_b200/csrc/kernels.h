@@ -167,7 +167,7 @@ struct KvGatherArgs {
   void *k_out = nullptr, *v_out = nullptr;
   int32_t *status = nullptr;
 };
-cudaError_t launch_kv_gather(const KvGatherArgs &a, bool bf16_out, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_gather(const KvGatherArgs &a, bool bf16_out, cudaStream_t s);
 
 struct KvAttnArgs {
   KvCache c;

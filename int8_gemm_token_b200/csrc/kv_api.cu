@@ -202,7 +202,7 @@ w8a8_status w8a8_kv_gather(const w8a8_kv_cache *cache, const int32_t *page_table
   a.v_out = v_out;
   int sms = 0;
   if (w8a8_status s = current_device_info(&sms, &a.status)) return s;
-  return from_cuda(launch_kv_gather(a, out_dtype == W8A8_BF16, sms, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_kv_gather(a, out_dtype == W8A8_BF16, static_cast<cudaStream_t>(stream)));
 }
 
 w8a8_status w8a8_kv_attention(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch, int64_t tokens, const void *q,

@@ -14,14 +14,19 @@
 //   Few new tokens a sequence (at most kFewTokens: decode steps): the group
 //   is one warp per (sequence, head, k or v), which walks the one or two
 //   pages its tokens touch.
-//   Many: the group is a block of 256 threads per page. Packed rows are cut
-//   into pages of their sequences by a search over
+//   Many: the group is 2 threads per token of a page (a warp for pages of 16,
+//   a block of 64 to 256 threads for the larger), so that a thread holds 64
+//   values whatever the page, all its loads in flight at once. Packed rows
+//   are cut into pages of their sequences by a search over
 //   f(b) = seq_start[b] / page + 2 b, which leaves each sequence room for
 //   the pages its tokens can touch (at most q / page + 2).
 // Within a group, D / 16 neighbouring threads hold one token: each takes the
 // two 8-element chunks of which one holds the first and one the second
 // elements of its pairs (or both whole pairs when interleaved), so a rotation
-// needs no exchange.
+// needs no exchange. Query rows are rotated by warps of their own, 4 passes
+// over the heads of a row at a time.
+//   The read-back takes a warp per (granule of 16 positions, head), whose
+// codes of k and of v are each one run of 16 D bytes.
 #include "kv_common.cuh"
 
 namespace w8a8 {
@@ -31,9 +36,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kFewTokens = 8;
 
-// 8 bf16 from global memory as fp32.
-__device__ __forceinline__ void load8(const uint16_t *p, float *x) {
-  const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+// 8 bf16 as fp32.
+__device__ __forceinline__ void widen8(const uint4 &v, float *x) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -100,30 +104,38 @@ template <int D, int G, int PASSES>
 __device__ __forceinline__ void append_unit(const KvAppendArgs &a, const KvSeq &seq, const int32_t *table_row, int pi,
                                             int lo, int hi, int h, int which, int tid, float *s_red) {
   constexpr int U = D / 16, TP = G / U;  // threads of a token, tokens of a pass
-  const int32_t page = load_page(table_row, pi, a.c.pages, a.status);
-  if (page < 0) return;  // uniform over the group: every thread read the same entry
   const KvRows &src = which ? a.v : a.k;
-  int8_t *codes = (which ? a.c.v : a.c.k) + ((static_cast<int64_t>(page) * a.c.heads + h) << a.c.page_shift) * D;
-  float *scale = (which ? a.c.vs : a.c.ks) + static_cast<int64_t>(page) * a.c.heads + h;
-  const int old = lo & (a.c.page - 1);  // tokens that lie in the page already
-  const float s_old = old > 0 ? *scale : 0.0f;
   const int u = tid % U, tok = tid / U;
   const bool turn = a.cos != nullptr && which == 0;
   const bool il = a.interleaved != 0;
   const int rot = turn ? a.rot : 0;
   int c0, c1;
   unit_chunks(u, rot, il, c0, c1);
+  uint4 raw[PASSES][2];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int pos = lo + p * TP + tok;
+    raw[p][0] = raw[p][1] = make_uint4(0, 0, 0, 0);
+    if (tok < TP && pos < hi) {
+      const uint16_t *row = src.p + (seq.row0 + pos - seq.pos0()) * src.token_stride + h * src.head_stride;
+      raw[p][0] = __ldg(reinterpret_cast<const uint4 *>(row + 8 * c0));
+      raw[p][1] = __ldg(reinterpret_cast<const uint4 *>(row + 8 * c1));
+    }
+  }
+  const int32_t page = load_page(table_row, pi, a.c.pages, a.status);
+  if (page < 0) return;  // uniform over the group: every thread read the same entry
+  int8_t *codes = (which ? a.c.v : a.c.k) + ((static_cast<int64_t>(page) * a.c.heads + h) << a.c.page_shift) * D;
+  float *scale = (which ? a.c.vs : a.c.ks) + static_cast<int64_t>(page) * a.c.heads + h;
+  const int old = lo & (a.c.page - 1);  // tokens that lie in the page already
+  const float s_old = old > 0 ? *scale : 0.0f;
   float x[PASSES][16];
   float amax = 0.0f;
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int pos = lo + p * TP + tok;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[p][i] = 0.0f;
+    widen8(raw[p][0], x[p]);
+    widen8(raw[p][1], x[p] + 8);
     if (tok < TP && pos < hi) {
-      const uint16_t *row = src.p + (seq.row0 + pos - seq.pos0()) * src.token_stride + h * src.head_stride;
-      load8(row + 8 * c0, x[p]);
-      load8(row + 8 * c1, x[p] + 8);
       if (16 * u < rot) {
         float cs[8], sn[8];
         const int64_t at = static_cast<int64_t>(pos) * (a.rot >> 1) + 8 * u;
@@ -168,11 +180,36 @@ __device__ __forceinline__ void append_unit(const KvAppendArgs &a, const KvSeq &
   if (tid == 0 && (old == 0 || S != s_old)) *scale = S;
 }
 
-// Rotation of one query row (all heads) by one warp; t a packed row.
+// Rotation of a part of the query rows by one warp: of the `w`-th (row, block
+// of kQueryPasses * 32 / (D / 16) heads).
+constexpr int kQueryPasses = 4;
+
 template <int D>
-__device__ __forceinline__ void rotate_query_row(const KvAppendArgs &a, int64_t t) {
+__host__ __device__ constexpr int query_heads() { return kQueryPasses * (32 / (D / 16)); }
+
+template <int D>
+__device__ __forceinline__ void rotate_query_rows(const KvAppendArgs &a, int64_t w) {
   constexpr int U = D / 16, HP = 32 / U;  // lanes of a head, heads of a pass
   const int lane = threadIdx.x & 31;
+  const int blocks = (a.q_heads + query_heads<D>() - 1) / query_heads<D>();
+  const int64_t t = w / blocks;
+  const int h0 = static_cast<int>(w - t * blocks) * query_heads<D>();
+  if (t >= a.s.tokens) return;
+  const int u = lane % U, hl = lane / U;
+  const bool il = a.interleaved != 0;
+  int c0, c1;
+  unit_chunks(u, a.rot, il, c0, c1);
+  uint4 raw[kQueryPasses][2];
+#pragma unroll
+  for (int p = 0; p < kQueryPasses; ++p) {
+    const int h = h0 + p * HP + hl;
+    raw[p][0] = raw[p][1] = make_uint4(0, 0, 0, 0);
+    if (hl < HP && h < a.q_heads) {
+      const uint16_t *row = a.q.p + t * a.q.token_stride + h * a.q.head_stride;
+      raw[p][0] = __ldg(reinterpret_cast<const uint4 *>(row + 8 * c0));
+      raw[p][1] = __ldg(reinterpret_cast<const uint4 *>(row + 8 * c1));
+    }
+  }
   const int32_t *next = a.s.seq_start + 1;
   const int32_t b = warp_count_le([&](int32_t i) { return static_cast<int64_t>(__ldg(next + i)); }, a.s.batch, t);
   if (b >= a.s.batch) return;  // behind the last sequence
@@ -180,10 +217,6 @@ __device__ __forceinline__ void rotate_query_row(const KvAppendArgs &a, int64_t 
   const int64_t i = t - seq.row0;
   if (i < 0 || i >= seq.q) return;
   const int64_t pos = seq.pos0() + i;
-  const int u = lane % U, hl = lane / U;
-  const bool il = a.interleaved != 0;
-  int c0, c1;
-  unit_chunks(u, a.rot, il, c0, c1);
   const bool turn = a.cos != nullptr && 16 * u < a.rot && pos >= 0;
   float cs[8], sn[8];
   if (turn) {
@@ -191,19 +224,16 @@ __device__ __forceinline__ void rotate_query_row(const KvAppendArgs &a, int64_t 
     load8f(a.cos + at, cs);
     load8f(a.sin + at, sn);
   }
-  if (hl >= HP) return;
-  for (int h = hl; h < a.q_heads; h += HP) {
-    const uint16_t *row = a.q.p + t * a.q.token_stride + h * a.q.head_stride;
-    uint16_t *out = a.q_out + (t * a.q_heads + h) * D;
-    float x[16];
-    if (pos >= 0) {
-      load8(row + 8 * c0, x);
-      load8(row + 8 * c1, x + 8);
-      if (turn) rotate16(x, cs, sn, il);
-    } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = 0.0f;
-    }
+  for (int p = 0; p < kQueryPasses; ++p) {
+    const int h = h0 + p * HP + hl;
+    if (hl >= HP || h >= a.q_heads) continue;
+    uint16_t *out = a.q_out + (t * a.q_heads + h) * D;
+    if (pos < 0) raw[p][0] = raw[p][1] = make_uint4(0, 0, 0, 0);
+    float x[16];
+    widen8(raw[p][0], x);
+    widen8(raw[p][1], x + 8);
+    if (turn) rotate16(x, cs, sn, il);
     *reinterpret_cast<uint4 *>(out + 8 * c0) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
                                                           pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
     *reinterpret_cast<uint4 *>(out + 8 * c1) = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]),
@@ -221,8 +251,7 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const __grid_const
   int64_t w = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
   const int64_t units = static_cast<int64_t>(a.s.batch) * a.c.heads * 2;
   if (w >= units) {
-    w -= units;
-    if (a.q_out && w < a.s.tokens) rotate_query_row<D>(a, w);
+    if (a.q_out) rotate_query_rows<D>(a, w - units);
     return;
   }
   const int which = static_cast<int>(w & 1);
@@ -240,23 +269,27 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const __grid_const
   }
 }
 
-// Many new tokens: blocks [0, tiles * heads * 2) one page of one head of k or
-// v each (blocks whose page does not exist leave), the following blocks 8
-// query rows each.
-template <int D>
-__global__ void __launch_bounds__(kThreads) append_pages_kernel(const __grid_constant__ KvAppendArgs a, int64_t tiles) {
-  __shared__ float s_red[kThreads / 32];
+// Many new tokens: units [0, tiles * heads * 2) are a page of a head of k or
+// v each, for G threads (units whose page does not exist are skipped); the
+// warps that follow them have query rows.
+template <int D, int G>
+__global__ void __launch_bounds__(G > 32 ? G : kThreads)
+    append_pages_kernel(const __grid_constant__ KvAppendArgs a, int64_t tiles) {
+  constexpr int BLOCK = G > 32 ? G : kThreads;
+  __shared__ float s_red[BLOCK / 32];
   pdl_launch_dependents();
   pdl_wait_prerequisite();
   const int64_t units = tiles * a.c.heads * 2;
-  if (blockIdx.x >= units) {
-    const int64_t t = (blockIdx.x - units) * (kThreads / 32) + (threadIdx.x >> 5);
-    if (t < a.s.tokens) rotate_query_row<D>(a, t);
+  const int64_t unit = (blockIdx.x * static_cast<int64_t>(BLOCK) + threadIdx.x) / G;
+  if (blockIdx.x == 0 && threadIdx.x < 32)  // every sequence is checked, the search may not come upon a bad one
+    for (int32_t i = threadIdx.x; i < a.s.batch; i += 32) load_seq(a.s, i, a.len_limit, a.status);
+  if (unit >= units) {
+    if (a.q_out) rotate_query_rows<D>(a, (unit - units) * (G / 32) + (threadIdx.x % G) / 32);
     return;
   }
   const int64_t per = a.c.heads * 2;
-  const int64_t tile = blockIdx.x / per;
-  const int which = static_cast<int>(blockIdx.x & 1), h = static_cast<int>((blockIdx.x % per) >> 1);
+  const int64_t tile = unit / per;
+  const int which = static_cast<int>(unit & 1), h = static_cast<int>((unit % per) >> 1);
   const int shift = a.c.page_shift;
   const auto f = [&](int32_t i) { return static_cast<int64_t>(__ldg(a.s.seq_start + i) >> shift) + 2 * int64_t(i); };
   const int32_t b = warp_count_le(f, a.s.batch, tile) - 1;
@@ -268,15 +301,15 @@ __global__ void __launch_bounds__(kThreads) append_pages_kernel(const __grid_con
   if (start >= seq.n || pi > ((seq.n - 1) >> shift)) return;
   const int lo = max(start, static_cast<int>(pi) << shift);
   const int hi = min(seq.n, static_cast<int>((pi + 1) << shift));
-  constexpr int TP = kThreads / (D / 16), PASSES = (128 + TP - 1) / TP;
-  append_unit<D, kThreads, PASSES>(a, seq, a.s.table + b * a.s.table_ld, static_cast<int>(pi), lo, hi, h, which,
-                                   threadIdx.x, s_red);
+  constexpr int TP = G / (D / 16), PASSES = (G / 2 + TP - 1) / TP;
+  append_unit<D, G, PASSES>(a, seq, a.s.table + b * a.s.table_ld, static_cast<int>(pi), lo, hi, h, which,
+                            threadIdx.x % G, s_red);
 }
 
-cudaLaunchConfig_t pdl_config(int64_t blocks, cudaStream_t s, cudaLaunchAttribute *attr) {
+cudaLaunchConfig_t pdl_config(int64_t blocks, int threads, cudaStream_t s, cudaLaunchAttribute *attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = s;
   attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr->val.programmaticStreamSerializationAllowed = 1;
@@ -286,28 +319,39 @@ cudaLaunchConfig_t pdl_config(int64_t blocks, cudaStream_t s, cudaLaunchAttribut
 }
 
 template <int D>
-cudaError_t launch_append_t(const KvAppendArgs &a, cudaStream_t s) {
+int64_t query_warps(const KvAppendArgs &a) {
+  return a.q_out ? a.s.tokens * ((a.q_heads + query_heads<D>() - 1) / query_heads<D>()) : 0;
+}
+
+template <int D, int G>
+cudaError_t launch_pages_t(const KvAppendArgs &a, cudaStream_t s) {
+  constexpr int BLOCK = G > 32 ? G : kThreads;
+  const int64_t tiles = (a.s.tokens >> a.c.page_shift) + 2 * static_cast<int64_t>(a.s.batch);
+  const int64_t threads = tiles * a.c.heads * 2 * G + query_warps<D>(a) * 32;
   cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = pdl_config((threads + BLOCK - 1) / BLOCK, BLOCK, s, &attr);
+  return cudaLaunchKernelEx(&cfg, append_pages_kernel<D, G>, a, tiles);
+}
+
+template <int D>
+cudaError_t launch_append_t(const KvAppendArgs &a, cudaStream_t s) {
   if (a.s.max_q <= kFewTokens) {
-    const int64_t warps = static_cast<int64_t>(a.s.batch) * a.c.heads * 2 + (a.q_out ? a.s.tokens : 0);
-    const cudaLaunchConfig_t cfg = pdl_config((warps + kThreads / 32 - 1) / (kThreads / 32), s, &attr);
+    const int64_t warps = static_cast<int64_t>(a.s.batch) * a.c.heads * 2 + query_warps<D>(a);
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = pdl_config((warps + kThreads / 32 - 1) / (kThreads / 32), kThreads, s, &attr);
     return cudaLaunchKernelEx(&cfg, append_few_kernel<D>, a);
   }
-  const int64_t tiles = (a.s.tokens >> a.c.page_shift) + 2 * static_cast<int64_t>(a.s.batch);
-  const int64_t blocks = tiles * a.c.heads * 2 + (a.q_out ? (a.s.tokens + kThreads / 32 - 1) / (kThreads / 32) : 0);
-  const cudaLaunchConfig_t cfg = pdl_config(blocks, s, &attr);
-  return cudaLaunchKernelEx(&cfg, append_pages_kernel<D>, a, tiles);
+  switch (a.c.page) {
+    case 16: return launch_pages_t<D, 32>(a, s);
+    case 32: return launch_pages_t<D, 64>(a, s);
+    case 64: return launch_pages_t<D, 128>(a, s);
+    default: return launch_pages_t<D, 256>(a, s);
+  }
 }
 
 // ------------------------------------------------------------------ gather
-// One warp per kGatherRows consecutive rows; lanes run over the row's 16-code
-// chunks (heads and, inside a head, neighbouring chunks), k and v alike.
-constexpr int kGatherRows = 4;
-
 template <bool BF16>
-__device__ __forceinline__ void gather_chunk(const int8_t *codes, float scale, void *out, int64_t elem, bool present) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (present) v = __ldg(reinterpret_cast<const uint4 *>(codes));
+__device__ __forceinline__ void store_values(const uint4 &v, float scale, void *out, int64_t elem) {
   float y[16];
   dequant16(v, scale, 0, y);
   if constexpr (BF16) {
@@ -322,43 +366,70 @@ __device__ __forceinline__ void gather_chunk(const int8_t *codes, float scale, v
   }
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ KvGatherArgs a) {
+__device__ __forceinline__ bool gather_ok(const KvGatherArgs &a, int32_t r0, int32_t r1, int32_t first) {
+  return r0 >= 0 && r1 >= r0 && r1 <= a.rows && first >= 0 &&
+         static_cast<int64_t>(first) + (r1 - r0) <= static_cast<int64_t>(a.max_pages) << a.c.page_shift;
+}
+
+// Warp (slot, head): the slot's granule of a sequence, found as a page is in
+// append_pages_kernel (f(b) = row_start[b] / 16 + 2 b).
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ KvGatherArgs a, int64_t warps) {
+  constexpr int C = D / 16, N = D / 32;  // 16-code chunks of a row; of k or of v to a lane
   pdl_launch_dependents();
   pdl_wait_prerequisite();
   const int lane = threadIdx.x & 31;
   const int64_t w = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
-  const int cpd = a.c.d >> 4, cpr = a.c.heads * cpd;  // 16-code chunks of a head and of a row
-  int32_t b = -1, r0 = 0, r1 = 0, first = 0;
-  bool ok = false;
-  for (int64_t t = w * kGatherRows; t < min(a.rows, (w + 1) * kGatherRows); ++t) {
-    if (b < 0 || t >= r1) {
-      const int32_t *next = a.row_start + 1;
-      b = warp_count_le([&](int32_t i) { return static_cast<int64_t>(__ldg(next + i)); }, a.batch, t);
-      if (b >= a.batch) return;
-      r0 = __ldg(a.row_start + b);
-      r1 = __ldg(a.row_start + b + 1);
-      first = __ldg(a.first_pos + b);
-      ok = r0 >= 0 && r0 <= t && t < r1 && r1 <= a.rows && first >= 0 &&
-           static_cast<int64_t>(first) + (r1 - r0) <= static_cast<int64_t>(a.max_pages) << a.c.page_shift;
-      if (!ok) record_error(a.status, W8A8_ERR_BAD_SEQUENCE);
+  if (w >= warps) return;
+  if (w == 0)  // as in append_pages_kernel
+    for (int32_t i = lane; i < a.batch; i += 32)
+      if (!gather_ok(a, __ldg(a.row_start + i), __ldg(a.row_start + i + 1), __ldg(a.first_pos + i)))
+        record_error(a.status, W8A8_ERR_BAD_SEQUENCE);
+  const int64_t slot = w / a.c.heads;
+  const int h = static_cast<int>(w - slot * a.c.heads);
+  const auto f = [&](int32_t i) { return static_cast<int64_t>(__ldg(a.row_start + i) / kGran) + 2 * int64_t(i); };
+  const int32_t b = warp_count_le(f, a.batch, slot) - 1;
+  if (b < 0) return;
+  const int32_t r0 = __ldg(a.row_start + b), r1 = __ldg(a.row_start + b + 1), first = __ldg(a.first_pos + b);
+  if (!gather_ok(a, r0, r1, first)) return;
+  const int64_t granule = first / kGran + (slot - f(b));
+  const int end = first + (r1 - r0);  // one past the last position
+  if (granule * kGran >= end) return;
+  const int key0 = static_cast<int>(granule) * kGran;
+  const int32_t page = load_page(a.table + b * a.table_ld, key0 >> a.c.page_shift, a.c.pages, a.status);
+  const int64_t block = static_cast<int64_t>(max(page, 0)) * a.c.heads + h;
+  const int64_t src = ((block << a.c.page_shift) + (key0 & (a.c.page - 1))) * D;
+  uint4 k[N], v[N];
+  float ks = 0.0f, vs = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) k[i] = v[i] = make_uint4(0, 0, 0, 0);  // a page that does not exist reads as 0
+  if (page >= 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t at = src + (i * 32 + lane) * 16;
+      if (a.k_out) k[i] = __ldg(reinterpret_cast<const uint4 *>(a.c.k + at));
+      if (a.v_out) v[i] = __ldg(reinterpret_cast<const uint4 *>(a.c.v + at));
     }
-    if (!ok) {
-      b = -1;
-      continue;
-    }
-    const int32_t pos = first + static_cast<int32_t>(t - r0);
-    const int32_t page = load_page(a.table + b * a.table_ld, pos >> a.c.page_shift, a.c.pages, a.status);
-    const int64_t block0 = static_cast<int64_t>(max(page, 0)) * a.c.heads;
-    for (int i = lane; i < cpr; i += 32) {
-      const int h = i / cpd, c = i - h * cpd;
-      const int64_t src = (((block0 + h) << a.c.page_shift) + (pos & (a.c.page - 1))) * a.c.d + 16 * c;
-      const int64_t dst = t * (static_cast<int64_t>(a.c.heads) * a.c.d) + 16 * i;
-      const bool here = page >= 0;
-      if (a.k_out) gather_chunk<BF16>(a.c.k + src, here ? __ldg(a.c.ks + block0 + h) : 0.0f, a.k_out, dst, here);
-      if (a.v_out) gather_chunk<BF16>(a.c.v + src, here ? __ldg(a.c.vs + block0 + h) : 0.0f, a.v_out, dst, here);
-    }
+    ks = __ldg(a.c.ks + block);
+    vs = __ldg(a.c.vs + block);
   }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int idx = i * 32 + lane, pos = key0 + idx / C;
+    if (pos < first || pos >= end) continue;
+    const int64_t elem = (static_cast<int64_t>(r0 + pos - first) * a.c.heads + h) * D + 16 * (idx % C);
+    if (a.k_out) store_values<BF16>(k[i], ks, a.k_out, elem);
+    if (a.v_out) store_values<BF16>(v[i], vs, a.v_out, elem);
+  }
+}
+
+template <int D>
+cudaError_t launch_gather_t(const KvGatherArgs &a, bool bf16_out, cudaStream_t s) {
+  const int64_t warps = (a.rows / kGran + 2 * static_cast<int64_t>(a.batch)) * a.c.heads;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = pdl_config((warps + kThreads / 32 - 1) / (kThreads / 32), kThreads, s, &attr);
+  if (bf16_out) return cudaLaunchKernelEx(&cfg, gather_kernel<D, true>, a, warps);
+  return cudaLaunchKernelEx(&cfg, gather_kernel<D, false>, a, warps);
 }
 
 }  // namespace
@@ -372,13 +443,13 @@ cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s) {
   }
 }
 
-cudaError_t launch_kv_gather(const KvGatherArgs &a, bool bf16_out, int num_sms, cudaStream_t s) {
-  (void)num_sms;
-  const int64_t warps = (a.rows + kGatherRows - 1) / kGatherRows;
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = pdl_config((warps + kThreads / 32 - 1) / (kThreads / 32), s, &attr);
-  if (bf16_out) return cudaLaunchKernelEx(&cfg, gather_kernel<true>, a);
-  return cudaLaunchKernelEx(&cfg, gather_kernel<false>, a);
+cudaError_t launch_kv_gather(const KvGatherArgs &a, bool bf16_out, cudaStream_t s) {
+  switch (a.c.d) {
+    case 64: return launch_gather_t<64>(a, bf16_out, s);
+    case 96: return launch_gather_t<96>(a, bf16_out, s);
+    case 128: return launch_gather_t<128>(a, bf16_out, s);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace w8a8

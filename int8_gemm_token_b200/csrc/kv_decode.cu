@@ -182,19 +182,32 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttnArgs &a, int32_t b, int3
   return w;
 }
 
-// Units before sequence `b` and all units; called by a whole warp. (Fewer
-// than 2^31 in all: the host has checked it.)
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if ((threadIdx.x & 31) >= o) v += u;
+  }
+  return v;
+}
+
+// Units before sequence `b` (if it is one) and all units; called by a whole
+// warp. Returns the lane's inclusive scan of the last 32 sequences. (Fewer
+// than 2^31 units in all: the host has checked it.)
 template <int ROWS>
-__device__ __forceinline__ void count_units(const KvAttnArgs &a, int32_t b, int32_t *status, uint32_t &before,
-                                            uint32_t &all) {
+__device__ __forceinline__ uint32_t count_units(const KvAttnArgs &a, int32_t b, int32_t *status, uint32_t &before,
+                                                uint32_t &all) {
   const int lane = threadIdx.x & 31;
+  uint32_t sum = 0;
   before = all = 0;
   for (int32_t i0 = 0; i0 < a.s.batch; i0 += 32) {
     const int32_t i = i0 + lane;
     const uint32_t v = i < a.s.batch ? seq_work<ROWS>(a, i, status).units() : 0;
-    if (b >= i0 && b < i0 + 32) before = all + __reduce_add_sync(0xFFFFFFFFu, i < b ? v : 0);
-    all += __reduce_add_sync(0xFFFFFFFFu, v);
+    sum = warp_scan(v);
+    if (b >= i0 && b < i0 + 32) before = all + __shfl_sync(0xFFFFFFFFu, sum - v, b - i0);
+    all += __shfl_sync(0xFFFFFFFFu, sum, 31);
   }
+  return sum;
 }
 
 // The sequence that unit `at` (of all) lies in, and the units before it.
@@ -205,12 +218,7 @@ __device__ __forceinline__ int32_t find_unit(const KvAttnArgs &a, uint32_t at, u
   for (int32_t i0 = 0; i0 < a.s.batch; i0 += 32) {
     const int32_t i = i0 + lane;
     const uint32_t v = i < a.s.batch ? seq_work<ROWS>(a, i, nullptr).units() : 0;
-    uint32_t sum = v;  // inclusive scan
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-      if (lane >= o) sum += u;
-    }
+    const uint32_t sum = warp_scan(v);
     const int32_t c = __popc(__ballot_sync(0xFFFFFFFFu, before + sum <= at));
     if (c < 32) {
       before += __shfl_sync(0xFFFFFFFFu, sum - v, c);
@@ -259,13 +267,19 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
 
   uint32_t all, before;
   const uint32_t p = warp * gridDim.x + blockIdx.x;  // few pieces spread over all SMs
-  count_units<ROWS>(a, -1, p == 0 ? a.status : nullptr, before, all);
+  const uint32_t sum = count_units<ROWS>(a, -1, p == 0 ? a.status : nullptr, before, all);
   if (all == 0) return;
   const Cut cut(all, gridDim.x * kWarps);
   if (p >= cut.pieces) return;
   uint32_t at = cut.begin(p);
   const uint32_t begin = at, end = cut.begin(p + 1);
-  int32_t b = find_unit<ROWS>(a, at, before);
+  int32_t b;
+  if (a.s.batch <= 32) {  // the scan of the one round is at hand
+    b = __popc(__ballot_sync(0xFFFFFFFFu, sum <= at));
+    before = b > 0 ? __shfl_sync(0xFFFFFFFFu, sum, b - 1) : 0;
+  } else {
+    b = find_unit<ROWS>(a, at, before);
+  }
   SeqWork work = seq_work<ROWS>(a, b, nullptr);
 
   const bool cap = a.softcap > 0.0f;
@@ -293,60 +307,24 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
     const int rows = seq.q * a.group, row0 = (seg - h * rbs) * ROWS;
     const int32_t *table_row = a.s.table + b * a.s.table_ld;
 
-    // this lane's query rows as the narrow operand of the scores (scaled into fp16's range), and as columns of S^T
+    // this lane's query rows, asked for before the pages
     uint32_t qf[NT][KS][2];
-    float slope[NT][2], mul[NT][2];
-    int pos[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = row0 + nt * 8 + g;
-      const bool ok = r < rows;
       const int i = r / a.group, hq = h * a.group + (r - i * a.group);
       const uint16_t *q = a.q.p + (seq.row0 + i) * a.q.token_stride + hq * a.q.head_stride;
-      uint32_t big = 0;  // bits of the row's largest magnitude
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint2 v = make_uint2(0, 0);
-        if (ok) v = __ldg(reinterpret_cast<const uint2 *>(q + k_dim<D>(t, k)));
+        if (r < rows) v = __ldg(reinterpret_cast<const uint2 *>(q + k_dim<D>(t, k)));
         qf[nt][k][0] = v.x;
         qf[nt][k][1] = v.y;
-        big = max(big, max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu)));
-      }
-      big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-      big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-      // 2^(14 - exponent of the largest), both ways; a zero row stays as it is
-      const int ex = min(max(static_cast<int>(big >> 7), 16), 254);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + 127 + 14 - ex > 254 ? 254 : 127 + 127 + 14 - ex) << 23);
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int z = 0; z < 2; ++z)
-          qf[nt][k][z] = pack_f16x2(bf16_lo(qf[nt][k][z]) * up, bf16_hi(qf[nt][k][z]) * up);
-      const float down = 1.0f / up;  // exact
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mul[nt][e] = __shfl_sync(0xFFFFFFFFu, down, 4 * (2 * t + e)) * score_mul;
-        const int rc = row0 + nt * 8 + 2 * t + e;
-        const int ic = rc / a.group;
-        pos[nt][e] = rc < rows ? seq.pos0() + ic : -1;
-        slope[nt][e] = a.slopes && rc < rows ? __ldg(a.slopes + h * a.group + (rc - ic * a.group)) * kLog2e : 0.0f;
       }
     }
     // positions of the first and last row (no row is hidden from keys at or before pos_min within the window)
     const int pos_min = seq.pos0() + row0 / a.group;
     const int pos_max = seq.pos0() + (min(row0 + ROWS, rows) - 1) / a.group;
-
-    float acc[MT][NT][4];
-    float m[NT][2], l[NT][2], mv[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) m[nt][e] = mv[nt][e] = -INFINITY, l[nt][e] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.0f;
-    }
 
     // Page, k's scale and log2 of v's scale of 32 tiles, one to a lane: of the
     // window that is being computed and, fetched when it begins, of the next.
@@ -380,6 +358,55 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
       }
       cp_async_commit();
     };
+
+    fetch(x0);
+    page_c = page_n, ks_c = ks_n, vs_c = vs_n;
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) load_tile(x0 + i, x0, i);
+    fetch(x0 + 32);
+
+    // the query rows as the narrow operand of the scores, scaled into fp16's range, and as columns of S^T
+    float slope[NT][2], mul[NT][2];
+    int pos[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      uint32_t big = 0;  // bits of the row's largest magnitude
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) big = max(big, max(qf[nt][k][z] & 0x7FFFu, (qf[nt][k][z] >> 16) & 0x7FFFu));
+      big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+      big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+      // 2^(14 - exponent of the largest) and back, exactly; a row of zeros stays one
+      const int ex = min(max(static_cast<int>(big >> 7), 16), 254);
+      const float up = __uint_as_float(static_cast<uint32_t>(min(127 + 127 + 14 - ex, 254)) << 23);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+          qf[nt][k][z] = pack_f16x2(bf16_lo(qf[nt][k][z]) * up, bf16_hi(qf[nt][k][z]) * up);
+      const float down = 1.0f / up;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mul[nt][e] = __shfl_sync(0xFFFFFFFFu, down, 4 * (2 * t + e)) * score_mul;
+        const int rc = row0 + nt * 8 + 2 * t + e;
+        const int ic = rc / a.group;
+        pos[nt][e] = rc < rows ? seq.pos0() + ic : -1;
+        slope[nt][e] = a.slopes && rc < rows ? __ldg(a.slopes + h * a.group + (rc - ic * a.group)) * kLog2e : 0.0f;
+      }
+    }
+
+    float acc[MT][NT][4];
+    float m[NT][2], l[NT][2], mv[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[nt][e] = mv[nt][e] = -INFINITY, l[nt][e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.0f;
+    }
 
     const auto compute_tile = [&](int x, int slot, int page, float k_scale, float v_log) {
       const uint8_t *ks = ring + slot * C::kStage, *vs = ks + kTile * C::kPitch;
@@ -499,11 +526,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
       }
     };
 
-    fetch(x0);
-    page_c = page_n, ks_c = ks_n, vs_c = vs_n;
-    fetch(x0 + 32);
-#pragma unroll
-    for (int i = 0; i < ST - 1; ++i) load_tile(x0 + i, x0, i);
     int win = x0, slot = 0;
 #pragma unroll 1
     for (int x = x0; x < x1; ++x) {
