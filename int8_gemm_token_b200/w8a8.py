@@ -596,6 +596,7 @@ def _same_gpu(dev: int, *ts):
 
 
 _entry = {}
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without making a Stream object
 
 
 def _kv_fn(name):
@@ -608,7 +609,12 @@ def _kv_fn(name):
 def _kv_call(fn, dev: int, stream, *args):
     """Call entry point `fn` with GPU `dev` current, on the given stream or the GPU's current one."""
     f = _kv_fn(fn)
-    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    if stream is not None:
+        raw = stream.cuda_stream
+    elif _current_raw_stream is not None:
+        raw = _current_raw_stream(dev)
+    else:
+        raw = torch.cuda.current_stream(dev).cuda_stream
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             status = f(*args, raw)
