@@ -173,7 +173,7 @@ __device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
 template <int D>
 __global__ void __launch_bounds__(kExpandThreads) kv_expand_kernel(const __grid_constant__ KvAttnArgs a,
                                                                    const __grid_constant__ Expanded x) {
-  constexpr int CH = D / 16, PITCH = PCfg<D>::kPitch;
+  constexpr int CH = D / 8, PITCH = PCfg<D>::kPitch;  // 8 codes to a lane: its 16-byte stores make one run
   __shared__ int32_t s_page[kExpandKeys / kGran];
   pdl_launch_dependents();
   pdl_wait_prerequisite();
@@ -204,19 +204,19 @@ __global__ void __launch_bounds__(kExpandThreads) kv_expand_kernel(const __grid_
   }
   __syncthreads();
   constexpr int N = (kExpandKeys * CH + kExpandThreads - 1) / kExpandThreads;
-  uint4 kv[N][2];  // every load of the thread in flight before the first is used
+  uint2 kv[N][2];  // every load of the thread in flight before the first is used
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const int i = n * kExpandThreads + threadIdx.x, r = i / CH, c = i - r * CH;
-    kv[n][0] = kv[n][1] = make_uint4(0, 0, 0, 0);
+    kv[n][0] = kv[n][1] = make_uint2(0, 0);
     if (r >= kExpandKeys) continue;
     const int key = key0 + r;
     const int32_t page = s_page[r / kGran];
     if (page < 0 || key >= seq.n) continue;
     const int64_t src =
-        (((static_cast<int64_t>(page) * a.c.heads + h) << a.c.page_shift) + (key & (a.c.page - 1))) * D + 16 * c;
-    kv[n][0] = __ldg(reinterpret_cast<const uint4 *>(a.c.k + src));
-    kv[n][1] = __ldg(reinterpret_cast<const uint4 *>(a.c.v + src));
+        (((static_cast<int64_t>(page) * a.c.heads + h) << a.c.page_shift) + (key & (a.c.page - 1))) * D + 8 * c;
+    kv[n][0] = __ldg(reinterpret_cast<const uint2 *>(a.c.k + src));
+    kv[n][1] = __ldg(reinterpret_cast<const uint2 *>(a.c.v + src));
   }
 #pragma unroll
   for (int n = 0; n < N; ++n) {
@@ -224,13 +224,10 @@ __global__ void __launch_bounds__(kExpandThreads) kv_expand_kernel(const __grid_
     if (r >= kExpandKeys) continue;
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-      const uint32_t w[4] = {kv[n][z].x, kv[n][z].y, kv[n][z].z, kv[n][z].w};
-      uint32_t o[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) codes_to_bf16(w[e], o[2 * e], o[2 * e + 1]);
-      uint4 *dst = reinterpret_cast<uint4 *>((z ? x.v : x.k) + (row0 + r) * PITCH + 16 * c);
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      uint4 o;
+      codes_to_bf16(kv[n][z].x, o.x, o.y);
+      codes_to_bf16(kv[n][z].y, o.z, o.w);
+      *reinterpret_cast<uint4 *>((z ? x.v : x.k) + (row0 + r) * PITCH + 8 * c) = o;
     }
   }
 }
