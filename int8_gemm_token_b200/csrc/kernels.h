@@ -187,7 +187,7 @@ bool kv_decode_fits(const KvAttnArgs &a);
 size_t kv_decode_workspace_bytes(const KvAttnArgs &a, int num_sms);
 cudaError_t launch_kv_decode(const KvAttnArgs &a, void *workspace, int num_sms, cudaStream_t s);
 bool kv_prefill_fits(const KvAttnArgs &a);
-size_t kv_prefill_workspace_bytes(const KvAttnArgs &a);
+size_t kv_prefill_workspace_bytes(const KvAttnArgs &a, int num_sms);
 cudaError_t launch_kv_prefill(const KvAttnArgs &a, void *workspace, int num_sms, cudaStream_t s);
 
 // Per-device set-up of the C ABI (done once per device): SM count and the

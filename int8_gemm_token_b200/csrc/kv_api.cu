@@ -102,7 +102,7 @@ w8a8_status check_attention_shape(const w8a8_kv_cache *cache, const w8a8_kv_batc
 }
 
 size_t workspace_bytes_of(const KvAttnArgs &a, int sms) {
-  return few_rows(a) ? kv_decode_workspace_bytes(a, sms) : kv_prefill_workspace_bytes(a);
+  return few_rows(a) ? kv_decode_workspace_bytes(a, sms) : kv_prefill_workspace_bytes(a, sms);
 }
 
 w8a8_status run_attention(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch, int64_t tokens, const void *q,

@@ -19,11 +19,14 @@
 //   fp16 has the codes' bits to spare but not bf16's range, so what meets them
 // is scaled by powers of two, exactly: a query row so that its largest
 // element is in [2^14, 2^15) (elements 2^-29 below it start to lose bits), and
-// the weights 2^s_j times v's scale against their own running maximum, apart
-// from that of the scores:
-//   mv = max_j (s_j + log2 vs_j),  w_j = 2^(s_j + log2 vs_j - mv) <= 1,
-//   out = 2^(mv - m) (sum_j w_j code_j) / l,  l = sum_j 2^(s_j - m) in fp32.
-// w_j is rounded to fp16 once (2^-11).
+// the weights 2^s_j times v's scale against a running reference of their own,
+// apart from that of the scores:
+//   w_j = 2^(s_j + log2 vs_j - mv),  l = sum_j 2^(s_j - m) in fp32,
+//   out = 2^(mv - m) (sum_j w_j code_j) / l.
+// w_j is rounded to fp16 once (2^-11). m and mv follow the maxima of s_j and of
+// s_j + log2 vs_j only when these have outgrown them by 2^8, which a vote over
+// the warp's elements finds; only then are maxima exchanged between lanes and
+// the sums rescaled (weights stay below 2^8 and so below fp16's largest).
 //   Both contractions may run over their axis in any order as long as both
 // sides use the same one, so a lane reads its codes of K as 16 contiguous
 // bytes of one key and those of V as the same dims of four keys (pairs of
@@ -50,6 +53,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = kGran;  // keys of a tile: one MMA's, of one page
+constexpr float kRescale = 8.0f;  // log2 of how far a maximum may outgrow its reference
 constexpr int kSetup = 4;     // what a segment's start costs, in tiles
 constexpr int kMinUnits = 8;  // of a piece
 constexpr int kJoinWarps = 4;
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
     float ks_c, vs_c, ks_n, vs_n;
     const auto fetch = [&](int x) {  // tiles x .. x + 31
       page_n = -1;
-      ks_n = 0.0f;
+      ks_n = -1.0f;  // (no page)
       vs_n = -INFINITY;
       if (x + lane >= x1) return;
       page_n = load_page(table_row, walk.tile(x + lane) * kTile >> a.c.page_shift, a.c.pages, a.status);
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
         for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.0f;
     }
 
-    const auto compute_tile = [&](int x, int slot, int page, float k_scale, float v_log) {
+    const auto compute_tile = [&](int x, int slot, float k_scale, float v_log) {
       const uint8_t *ks = ring + slot * C::kStage, *vs = ks + kTile * C::kPitch;
       const int key0 = walk.tile(x) * kTile;
       float s[NT][4];
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
         }
       }
       // scores, in units of log2; element e of s[nt]: key g + 8 (e >> 1), row 2 t + (e & 1)
-      const bool whole = key0 + kTile - 1 <= pos_min && (a.window == 0 || key0 > pos_max - a.window) && page >= 0;
+      const bool whole = key0 + kTile - 1 <= pos_min && (a.window == 0 || key0 > pos_max - a.window) && k_scale != -1.0f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
             const int j = key0 + g + 8 * (e >> 1), at_q = pos[nt][e & 1];
             float v = s[nt][e] + slope[nt][e & 1] * static_cast<float>(j - at_q);
             if (!whole) {
-              const bool seen = page >= 0 && j < seq.n && at_q >= 0 &&
+              const bool seen = k_scale != -1.0f && j < seq.n && at_q >= 0 &&
                                 ((j <= at_q && (a.window == 0 || at_q - j < a.window)) || j < prefix);
               v = seen ? v : -INFINITY;
               any = any || seen;
@@ -461,37 +465,37 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
         // a page of which no row sees anything may hold anything: it adds nothing
         if (!__any_sync(0xFFFFFFFFu, any)) return;
       }
+      float top[NT][2];
       bool grew = false;
-      float al[NT][2], fv[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float v = fmaxf(s[nt][e], s[nt][e + 2]);
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-          al[nt][e] = 1.0f;
-          if (v > m[nt][e]) {
-            l[nt][e] *= ex2(m[nt][e] - v);
-            m[nt][e] = v;
-          }
-          if (v + v_log > mv[nt][e]) {
-            al[nt][e] = ex2(mv[nt][e] - (v + v_log));
-            mv[nt][e] = v + v_log;
-            grew = true;
-          }
-          // from 2^(s - m) to w (its exponent held in range: it is large only
-          // where 2^(s - m) is 0); 0 for a row that sees nothing of the page
-          const float x = m[nt][e] + v_log - mv[nt][e];
-          fv[nt][e] = v == -INFINITY || mv[nt][e] == -INFINITY ? 0.0f : ex2(x > 126.0f ? 126.0f : x);
+          top[nt][e] = fmaxf(s[nt][e], s[nt][e + 2]);
+          grew = grew || top[nt][e] > m[nt][e] + kRescale || top[nt][e] + v_log > mv[nt][e] + kRescale;
         }
       if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
+          for (int e = 0; e < 2; ++e) {
+            float v = top[nt][e];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][nt][e] *= al[nt][e & 1];
+            for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+            if (v > m[nt][e]) {
+              l[nt][e] *= ex2(m[nt][e] - v);
+              m[nt][e] = v;
+            }
+            if (v + v_log > mv[nt][e]) {
+              const float al = ex2(mv[nt][e] - (v + v_log));
+              mv[nt][e] = v + v_log;
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                acc[i][nt][e] *= al;
+                acc[i][nt][e + 2] *= al;
+              }
+            }
+          }
       }
       uint32_t ph[NT][2];
 #pragma unroll
@@ -502,7 +506,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
           const float ref = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];  // a row that has seen no key yet
           w[e] = ex2(s[nt][e] - ref);
           l[nt][e & 1] += w[e];
-          w[e] *= fv[nt][e & 1];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // from 2^(s - m) to w (its exponent held in range: it is large only
+          // where 2^(s - m) is 0); a weight of 0 stays one whatever the page's scale
+          const float x = m[nt][e] + v_log - mv[nt][e];
+          const float fv = mv[nt][e] == -INFINITY ? 0.0f : ex2(x > 126.0f ? 126.0f : x);
+          w[e] = whole || w[e] > 0.0f ? w[e] * fv : 0.0f;
+          w[e + 2] = whole || w[e + 2] > 0.0f ? w[e + 2] * fv : 0.0f;
         }
         ph[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
         ph[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
@@ -537,8 +549,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
       cp_async_wait<ST - 2>();
       __syncwarp();  // every lane's copies of this tile have landed, and all have read the slot loaded next
       load_tile(x + ST - 1, win, slot == 0 ? ST - 1 : slot - 1);
-      compute_tile(x, slot, __shfl_sync(0xFFFFFFFFu, page_c, x - win), __shfl_sync(0xFFFFFFFFu, ks_c, x - win),
-                   __shfl_sync(0xFFFFFFFFu, vs_c, x - win));
+      compute_tile(x, slot, __shfl_sync(0xFFFFFFFFu, ks_c, x - win), __shfl_sync(0xFFFFFFFFu, vs_c, x - win));
       slot = slot + 1 == ST ? 0 : slot + 1;
     }
     cp_async_wait<0>();

@@ -83,37 +83,51 @@ int64_t expanded_len(int32_t max_kv) { return (static_cast<int64_t>(max_kv) + kK
 constexpr int kExpandKeys = 64;
 constexpr int kExpandThreads = 256;
 
-// A query block: its first packed row, the position of that row's token, its
-// tokens (of 2 floor(128 / group) at most), and its sequence.
+// A query block, or a part of one: its first packed row, the position of that
+// row's token, its tokens (of 2 floor(128 / group) at most), its sequence, the
+// part [x0, x1) of the key tiles it walks, and where a part leaves its sums.
 struct __align__(16) QueryBlock {
   int32_t row, pos, toks, b;
-  int32_t n, prefix, pad0, pad1;
+  int32_t n, prefix, x0, x1;
+  int32_t slot;   // of parts: slot * kv heads + head in the workspace; -1: the block is whole
+  int32_t parts;  // in the list of split blocks: how many, from `slot` on
+  int32_t pad[2];
 };
 
 struct Expanded {
   uint16_t *k, *v;      // [sequence][head][len][pitch]
   float *ks, *vs;       // [sequence][head][len / 16]
   int64_t len;
-  int32_t *counters;    // [0] query blocks listed, [1] items taken
-  QueryBlock *blocks;   // those with the most key tiles first
-  int32_t slots;        // room in the list
+  int32_t *counters;    // [0] entries listed, [1] items taken, [2] blocks split
+  QueryBlock *blocks;   // blocks and parts, those with the most key tiles first
+  QueryBlock *split;    // blocks in parts
+  float *parts;         // [slot][kv head]: sums [2][128][D], then (maximum, sum of weights) [2][128][2]
+  int32_t slots;        // query blocks there may be
+  int32_t most_parts;   // parts there may be (0: blocks stay whole)
+  int32_t sms;
 };
 
 // The list of query blocks, by one block of kExpandThreads threads: a counting
 // sort by the number of key tiles, descending. Slot f(b) = seq_start[b] / T + b
 // leaves sequence b room for its ceil(q / T) blocks of T tokens. The order of
-// blocks with equally many tiles is left open; it decides only where and when
-// a block runs.
+// entries with equally many tiles is left open; it decides only where and when
+// one runs.
+//   Where there are few blocks (the host allows parts), one with many more key
+// tiles than an even share of all of them over the SMs is split into parts of
+// at most that share. Parts of split blocks are at most twice the SMs: each
+// split block has more than a share, so ceil(count / share) < 2 count / share.
 constexpr int kBins = 2048;
+constexpr int kMinShare = 4;
 
 __device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
-  __shared__ int32_t s_bin[kBins], s_sum[kExpandThreads];
+  __shared__ int32_t s_bin[kBins], s_sum[kExpandThreads], s_count[3];  // all tiles; split blocks; parts
   const int T = 2 * (kRows / a.group), tid = threadIdx.x;
   int shift = 0;
   while ((x.len / kKeys) >> shift >= kBins) ++shift;
   for (int i = tid; i < kBins; i += kExpandThreads) s_bin[i] = 0;
+  if (tid < 3) s_count[tid] = 0;
   __syncthreads();
-  const auto block_of = [&](int32_t slot, QueryBlock &q, int &bin) {
+  const auto block_of = [&](int32_t slot, QueryBlock &q) {
     int lo = 0, hi = a.s.batch;  // the last sequence whose slots begin at or before this one
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
@@ -133,15 +147,34 @@ __device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
     q.toks = min(T, seq.q - static_cast<int>(tok));
     q.n = seq.n;
     q.prefix = a.prefix ? __ldg(a.prefix + b) : 0;
-    q.pad0 = q.pad1 = 0;
-    const int tiles = tile_walk(kKeys, q.prefix, q.n, max(q.pos, 0), q.pos + q.toks, a.window).count;
-    bin = kBins - 1 - min(tiles >> shift, kBins - 1);
+    q.x0 = 0;
+    q.x1 = tile_walk(kKeys, q.prefix, q.n, max(q.pos, 0), q.pos + q.toks, a.window).count;
+    q.slot = -1;
+    q.parts = 1;
+    q.pad[0] = q.pad[1] = 0;
     return true;
   };
   QueryBlock q;
-  int bin = 0;
+  int share = INT32_MAX;
+  if (x.most_parts > 0) {
+    int sum = 0;
+    for (int slot = tid; slot < x.slots; slot += kExpandThreads)
+      if (block_of(slot, q)) sum += q.x1;
+    atomicAdd(&s_count[0], sum);
+    __syncthreads();
+    const int64_t all = static_cast<int64_t>(s_count[0]) * a.c.heads;
+    share = max(kMinShare, static_cast<int>((all + x.sms - 1) / x.sms));
+  }
+  // (a part more costs about 4 tiles and the join as much: not for a few tiles over the share)
+  const auto parts_of = [&](int count) {
+    return share < INT32_MAX && count > share + max(8, share / 2) ? (count + share - 1) / share : 1;
+  };
+  const auto bin_of = [&](int tiles) { return kBins - 1 - min(tiles >> shift, kBins - 1); };
   for (int slot = tid; slot < x.slots; slot += kExpandThreads)
-    if (block_of(slot, q, bin)) atomicAdd(&s_bin[bin], 1);
+    if (block_of(slot, q)) {
+      const int parts = parts_of(q.x1), per = (q.x1 + parts - 1) / parts;
+      for (int i = 0; i < parts; ++i) atomicAdd(&s_bin[bin_of(min(per, q.x1 - i * per))], 1);
+    }
   __syncthreads();
   // exclusive scan of the bins, kBins / kExpandThreads to a thread
   constexpr int PER = kBins / kExpandThreads;
@@ -167,11 +200,27 @@ __device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
   }
   __syncthreads();
   for (int slot = tid; slot < x.slots; slot += kExpandThreads)
-    if (block_of(slot, q, bin)) x.blocks[atomicAdd(&s_bin[bin], 1)] = q;
+    if (block_of(slot, q)) {
+      const int count = q.x1, parts = parts_of(count), per = (count + parts - 1) / parts;
+      if (parts > 1) {
+        q.slot = atomicAdd(&s_count[2], parts);
+        q.parts = parts;
+        x.split[atomicAdd(&s_count[1], 1)] = q;
+      }
+      const int slot0 = q.slot;
+      for (int i = 0; i < parts; ++i) {
+        if (parts > 1) q.slot = slot0 + i;
+        q.x0 = i * per;
+        q.x1 = min(count, q.x0 + per);
+        x.blocks[atomicAdd(&s_bin[bin_of(q.x1 - q.x0)], 1)] = q;
+      }
+    }
+  __syncthreads();
+  if (tid == 0) x.counters[2] = s_count[1];
 }
 
 template <int D>
-__global__ void __launch_bounds__(kExpandThreads) kv_expand_kernel(const __grid_constant__ KvAttnArgs a,
+__global__ void __launch_bounds__(kExpandThreads, 6) kv_expand_kernel(const __grid_constant__ KvAttnArgs a,
                                                                    const __grid_constant__ Expanded x) {
   constexpr int CH = D / 8, PITCH = PCfg<D>::kPitch;  // 8 codes to a lane: its 16-byte stores make one run
   __shared__ int32_t s_page[kExpandKeys / kGran];
@@ -269,6 +318,10 @@ struct Item {
   int32_t h, pad[3];
 };
 
+// Floats of a part's sums and of its rows' (maximum, sum of weights).
+template <int D>
+constexpr int part_floats() { return 2 * kRows * (D + 2); }
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -334,13 +387,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int tpt = kRows / a.group;  // tokens of a tile
 
-  // Tokens of an item's tile A (t = 0) or B, the key tiles it walks, and the
-  // walk. Both tiles walk from the item's first key, so one walk is a prefix
-  // of the other.
+  // Tokens of an item's tile A (t = 0) or B, the key tiles it walks (from
+  // number x0 of the walk), and the walk. Both tiles walk from the block's
+  // first key, so one walk is a prefix of the other.
   const auto toks_of = [&](const QueryBlock &q, int t) { return max(0, min(tpt, q.toks - t * tpt)); };
   const auto count_of = [&](const QueryBlock &q, int t) {
     const int toks = toks_of(q, t), last = q.pos + t * tpt + toks;  // one past its last position
-    return toks > 0 && last > 0 ? tile_walk(kKeys, q.prefix, q.n, max(q.pos, 0), last, a.window).count : 0;
+    const int count = toks > 0 && last > 0 ? tile_walk(kKeys, q.prefix, q.n, max(q.pos, 0), last, a.window).count : 0;
+    return max(0, min(count, q.x1) - q.x0);
   };
   const auto walk_of = [&](const QueryBlock &q) {
     return tile_walk(kKeys, q.prefix, q.n, max(q.pos, 0), q.n, a.window);
@@ -403,10 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const TileWalk walk = walk_of(item.q);
           const int most = max(count_of(item.q, 0), count_of(item.q, 1));
           const int64_t key0 = (static_cast<int64_t>(item.q.b) * a.c.heads + item.h) * x.len;
-          if (most > 0) load(&tmK, key0 + walk.tile(0) * kKeys);
+          const int x0 = item.q.x0;
+          if (most > 0) load(&tmK, key0 + walk.tile(x0) * kKeys);
           for (int j = 0; j < most && ok; ++j) {
-            load(&tmV, key0 + walk.tile(j) * kKeys);
-            if (j + 1 < most) load(&tmK, key0 + walk.tile(j + 1) * kKeys);
+            load(&tmV, key0 + walk.tile(x0 + j) * kKeys);
+            if (j + 1 < most) load(&tmK, key0 + walk.tile(x0 + j + 1) * kKeys);
           }
         }
         if (!ok) {
@@ -553,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t steps = 0, outs = 0;  // score tiles and outputs of this query tile so far
     Item item;
     for (int it = 0; take(it, item, ok); ++it) {
-    const int toks = toks_of(item.q, w), count = count_of(item.q, w), n = item.q.n, prefix = item.q.prefix;
+    const int toks = toks_of(item.q, w), count = count_of(item.q, w), n = item.q.n, prefix = item.q.prefix, x0 = item.q.x0;
+    const int slot = item.q.slot < 0 ? -1 : item.q.slot * a.c.heads + item.h;
     const TileWalk walk = walk_of(item.q);
     const int row0 = item.q.row + w * tpt, h0 = item.h * a.group;
     const int pos_min = item.q.pos + w * tpt, pos_max = pos_min + toks - 1;
@@ -565,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -INFINITY, l = 0.0f;
     const float *ks = x.ks + krow / kGran, *vs = x.vs + krow / kGran;
     for (int j = 0; j < count; ++j) {
-      const int key0 = walk.tile(j) * kKeys;
+      const int key0 = walk.tile(x0 + j) * kKeys;
       float kc[8], vc[8];  // scales of the tile's granules
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -740,6 +796,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&o_bar[w], outs & 1u, abort_flag, limit_ns));
     if (!ok) break;
     tc_fence_after();
+    if (slot >= 0) {  // a part: its sums, maximum and sum of weights
+      float *const part = x.parts + static_cast<int64_t>(slot) * part_floats<D>();
+      *reinterpret_cast<float2 *>(part + 2 * kRows * D + (w * kRows + row) * 2) = make_float2(count > 0 ? m : -INFINITY, l);
+      if (count > 0) {
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          tmem_ld_32x32b_x16(t_o + 16 * c, o);
+          tmem_ld_wait();
+          // dims by 4, rows side by side: a warp's stores are runs of 512 bytes
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4 *>(part + (static_cast<int64_t>(w * (D / 4) + 4 * c + e) * kRows + row) * 4) =
+                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      tc_fence_before();
+      steps += static_cast<uint32_t>(count);
+      outs += count > 0 ? 1u : 0u;
+      continue;
+    }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     const float r_out = a.r_out ? __ldg(a.r_out) : 0.0f;
     const int z_out = a.r_out ? __ldg(a.z_out) : 0;
@@ -825,27 +902,77 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Joins the parts of split blocks, in their order: a warp per 4 dims of 32
+// neighbouring rows.
+constexpr int kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) kv_prefill_join_kernel(const __grid_constant__ KvAttnArgs a,
+                                                                       const __grid_constant__ Expanded x) {
+  pdl_launch_dependents();
+  pdl_wait_prerequisite();
+  const int tpt = kRows / a.group, lane = threadIdx.x & 31;
+  const int64_t units = static_cast<int64_t>(x.counters[2]) * a.c.heads * (2 * kRows / 32) * (D / 4);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kJoinThreads / 32);
+  for (int64_t u = blockIdx.x * static_cast<int64_t>(kJoinThreads / 32) + (threadIdx.x >> 5); u < units; u += stride) {
+    const int d4 = static_cast<int>(u % (D / 4));
+    const int64_t v = u / (D / 4);
+    const int rows32 = static_cast<int>(v % (2 * kRows / 32)), h = static_cast<int>(v / (2 * kRows / 32) % a.c.heads);
+    const QueryBlock &q = x.split[v / (2 * kRows / 32) / a.c.heads];
+    const int w = rows32 / (kRows / 32), row = (rows32 % (kRows / 32)) * 32 + lane;  // tile and row in it
+    const int tok = row / a.group;
+    if (tok >= tpt || w * tpt + tok >= q.toks) continue;
+    float m = -INFINITY, l = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < q.parts; ++i) {
+      const float *part = x.parts + (static_cast<int64_t>(q.slot + i) * a.c.heads + h) * part_floats<D>();
+      const float2 ml = *reinterpret_cast<const float2 *>(part + 2 * kRows * D + (w * kRows + row) * 2);
+      if (ml.x == -INFINITY) continue;
+      const float4 o = *reinterpret_cast<const float4 *>(part + (static_cast<int64_t>(w * (D / 4) + d4) * kRows + row) * 4);
+      const float m2 = fmaxf(m, ml.x), f0 = ex2(m - m2), f1 = ex2(ml.x - m2);
+      m = m2;
+      l = l * f0 + ml.y * f1;
+      y[0] = y[0] * f0 + o.x * f1, y[1] = y[1] * f0 + o.y * f1, y[2] = y[2] * f0 + o.z * f1, y[3] = y[3] * f0 + o.w * f1;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] *= inv;
+    const int hq = h * a.group + row - tok * a.group;
+    store_out4(a, (static_cast<int64_t>(q.row + w * tpt + tok) * a.q_heads + hq) * D + 4 * d4, y);
+  }
+}
+
 int64_t query_block_slots(const KvAttnArgs &a) { return a.s.tokens / (2 * (kRows / a.group)) + a.s.batch; }
 
-Expanded expanded_of(const KvAttnArgs &a, void *workspace) {
+// Whether blocks may be split: where there are not many more items than SMs.
+// (Measured: with 8 items an SM the longest-first order alone leaves the SMs
+// within 3 % of one another; with 2, an SM may wait for one item half the time.)
+bool may_split(const KvAttnArgs &a, int num_sms) { return query_block_slots(a) * a.c.heads <= 4 * num_sms; }
+
+int64_t part_bytes(const KvAttnArgs &a) { return int64_t(2) * kRows * (a.c.d + 2) * sizeof(float); }
+
+Expanded expanded_of(const KvAttnArgs &a, void *workspace, int num_sms) {
   Expanded x;
   x.len = expanded_len(a.s.max_kv);
   x.slots = static_cast<int32_t>(query_block_slots(a));
+  x.sms = num_sms;
+  x.most_parts = may_split(a, num_sms) ? 2 * num_sms : 0;  // over all heads
   const int64_t keys = static_cast<int64_t>(a.s.batch) * a.c.heads * x.len;
   const int64_t pitch = a.c.d > 64 ? 128 : 64;
   x.k = static_cast<uint16_t *>(workspace);
   x.v = x.k + keys * pitch;
   x.ks = reinterpret_cast<float *>(x.v + keys * pitch);
   x.vs = x.ks + keys / kGran;
-  x.blocks = reinterpret_cast<QueryBlock *>(x.vs + keys / kGran);
-  x.counters = reinterpret_cast<int32_t *>(x.blocks + x.slots);
+  x.parts = x.vs + keys / kGran;
+  x.blocks = reinterpret_cast<QueryBlock *>(reinterpret_cast<char *>(x.parts) + x.most_parts * part_bytes(a));
+  x.split = x.blocks + x.slots + x.most_parts;
+  x.counters = reinterpret_cast<int32_t *>(x.split + (x.most_parts ? x.slots : 0));
   return x;
 }
 
 template <int D>
 cudaError_t launch_t(const KvAttnArgs &a, void *workspace, int num_sms, cudaStream_t s) {
   using C = PCfg<D>;
-  const Expanded x = expanded_of(a, workspace);
+  const Expanded x = expanded_of(a, workspace, num_sms);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -875,11 +1002,16 @@ cudaError_t launch_t(const KvAttnArgs &a, void *workspace, int num_sms, cudaStre
   if (e != cudaSuccess) return e;
   e = ensure_kernel_smem<kv_prefill_kernel<D>>(static_cast<int>(C::kSmem), false);
   if (e != cudaSuccess) return e;
-  const int64_t items = static_cast<int64_t>(x.slots) * a.c.heads;
+  const int64_t items = static_cast<int64_t>(x.slots + x.most_parts) * a.c.heads;
   cfg.gridDim = dim3(static_cast<unsigned>(items < num_sms ? items : num_sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
-  return cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D>, tmQ, tmK, tmV, tmOut, a, x, kWaitLimitNs);
+  e = cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D>, tmQ, tmK, tmV, tmOut, a, x, kWaitLimitNs);
+  if (e != cudaSuccess || x.most_parts == 0) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms) * 4);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, kv_prefill_join_kernel<D>, a, x);
 }
 
 }  // namespace
@@ -890,10 +1022,9 @@ bool kv_prefill_fits(const KvAttnArgs &a) {
   return rows <= INT32_MAX && query_block_slots(a) * a.c.heads <= INT32_MAX / 2;
 }
 
-size_t kv_prefill_workspace_bytes(const KvAttnArgs &a) {
-  const size_t keys = static_cast<size_t>(a.s.batch) * a.c.heads * expanded_len(a.s.max_kv);
-  return keys * ((a.c.d > 64 ? 128 : 64) * 2 * sizeof(uint16_t)) + keys / kGran * 2 * sizeof(float) +
-         static_cast<size_t>(query_block_slots(a)) * sizeof(QueryBlock) + 16;
+size_t kv_prefill_workspace_bytes(const KvAttnArgs &a, int num_sms) {
+  const Expanded x = expanded_of(a, nullptr, num_sms);
+  return reinterpret_cast<uintptr_t>(x.counters) + 16;
 }
 
 cudaError_t launch_kv_prefill(const KvAttnArgs &a, void *workspace, int num_sms, cudaStream_t s) {

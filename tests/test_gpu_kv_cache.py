@@ -242,6 +242,15 @@ def test_attention_chunks(d, page, hq, hkv, new, ctx):
     check_attention(rng, s, R.random_cache(rng, pages, hkv, page, d), hq)
 
 
+@pytest.mark.parametrize("d,page,hq,hkv", [(128, 64, 4, 1), (96, 16, 3, 1), (64, 32, 4, 4)])
+@pytest.mark.parametrize("mask", ["plain", "window_prefix", "all"])
+def test_attention_few_long_blocks(d, page, hq, hkv, mask):
+    """Few query blocks behind long contexts: their key tiles are split over the SMs and joined."""
+    rng = np.random.default_rng(d)
+    s, pages = R.make_seqs(rng, [70, 40, 300], [5000, 3, 1500], page, spare=1)
+    check_attention(rng, s, R.random_cache(rng, pages, hkv, page, d), hq, **mask_args(mask, hq))
+
+
 @pytest.mark.parametrize("new,kv", [([1, 1, 1], [0, 5, 0]), ([3, 2], [1, 0]), ([50, 70, 40], [30, 70, 0])])
 @pytest.mark.parametrize("prefix", [None, [4, 4, 4]])
 def test_attention_padding_rows_are_zero(new, kv, prefix):
