@@ -8,7 +8,7 @@
 // with scores in units of log2.
 //
 // How: the bound is the cache's bytes from HBM, each used once for all the
-// query rows of its kv head, so a warp takes 16 keys at a time and the rows
+// query rows of its kv head, so a warp takes 32 keys at a time and the rows
 // (group * new tokens) are the narrow side of the products: S^T = K Q^T with
 // 16 keys x 8 rows x 16 dims an instruction, and O^T = V^T P^T with 16 dims x
 // 8 rows x 16 keys. Those shapes are mma.sync's; tcgen05 wants 128 rows of
@@ -37,7 +37,7 @@
 // waits for nobody; the stages are swizzled so that both reads are free of
 // bank conflicts (D = 128).
 //
-// Work: the key tiles (16 keys) of all segments -- (sequence, kv head, block
+// Work: the key tiles (32 keys) of all segments -- (sequence, kv head, block
 // of query rows) -- laid end to end, each with kSetup units more for its
 // start, are cut into equal pieces, one to a warp, whatever the lengths of
 // the sequences, which only the device knows. A warp that holds all of a
@@ -52,21 +52,24 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = kGran;  // keys of a tile: one MMA's, of one page
+constexpr int kTile = 32;     // keys of a tile: two granules, each of one page
 constexpr float kRescale = 8.0f;  // log2 of how far a maximum may outgrow its reference
-constexpr int kSetup = 4;     // what a segment's start costs, in tiles
-constexpr int kMinUnits = 8;  // of a piece
+constexpr int kSetup = 2;     // what a segment's start costs, in tiles
+constexpr int kMinUnits = 4;  // of a piece
 constexpr int kJoinWarps = 4;
 
-// Blocks of an SM and stages of a warp's ring: with 8 query rows 16 warps of
-// 128 registers, with 16 rows (twice the sums and queries in registers) 12.
-template <int D, int NT>
+// 12 warps of 168 registers an SM, each with two stages of a tile: while one
+// is computed with, the other's 8 KiB are in flight, 96 KiB an SM. (16 warps of
+// 128 registers with tiles of 16 keys kept 128 KiB in flight and were slower:
+// what is done once a tile, whatever its keys, cost them 100 of 450 instructions.)
+constexpr int kBlocks = 3;
+constexpr int kStages = 2;
+
+template <int D>
 struct Cfg {
   static constexpr int kPitch = D == 64 ? 64 : 128;        // bytes of a key's row in a stage
   static constexpr int kStage = 2 * kTile * kPitch;        // K rows, then V rows
   static constexpr int kChunks = D / 16;
-  static constexpr int kBlocks = NT == 1 ? 4 : 3;
-  static constexpr int kStages = NT == 1 ? 3 : 4;
   static constexpr size_t kSmem = static_cast<size_t>(kWarps) * kStages * kStage;
   static_assert(kBlocks * (kSmem + 1024) <= 227 * 1024, "shared memory per SM");
 };
@@ -256,18 +259,17 @@ template <int D, int NT>
 constexpr int partial_floats() { return 8 * NT * (D + 4); }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
+__global__ void __launch_bounds__(kThreads, kBlocks)
     kv_decode_kernel(const __grid_constant__ KvAttnArgs a, float *__restrict__ partial) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D>;
   constexpr int KS = D / 16;   // contraction steps of the scores
   constexpr int MT = D / 16;   // 16-dim tiles of the output
   constexpr int ROWS = 8 * NT;
-  constexpr int ST = C::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   pdl_wait_prerequisite();
   pdl_launch_dependents();  // after the wait: the join may read the lengths before its own
-  uint8_t *ring = smem + warp * (ST * C::kStage);
+  uint8_t *ring = smem + warp * (kStages * C::kStage);
 
   uint32_t all, before;
   const uint32_t p = warp * gridDim.x + blockIdx.x;  // few pieces spread over all SMs
@@ -330,16 +332,18 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
     const int pos_min = seq.pos0() + row0 / a.group;
     const int pos_max = seq.pos0() + (min(row0 + ROWS, rows) - 1) / a.group;
 
-    // Page, k's scale and log2 of v's scale of 32 tiles, one to a lane: of the
-    // window that is being computed and, fetched when it begins, of the next.
+    // Page, k's scale and log2 of v's scale of 32 granules (16 tiles), one to
+    // a lane: of the window that is being computed and, fetched when it
+    // begins, of the next.
     int page_c, page_n;
     float ks_c, vs_c, ks_n, vs_n;
-    const auto fetch = [&](int x) {  // tiles x .. x + 31
+    const auto fetch = [&](int x) {  // tiles x .. x + 15
       page_n = -1;
       ks_n = -1.0f;  // (no page)
       vs_n = -INFINITY;
-      if (x + lane >= x1) return;
-      page_n = load_page(table_row, walk.tile(x + lane) * kTile >> a.c.page_shift, a.c.pages, a.status);
+      const int key = walk.tile(x + (lane >> 1)) * kTile + (lane & 1) * kGran;
+      if (x + (lane >> 1) >= x1 || key >= seq.n) return;
+      page_n = load_page(table_row, key >> a.c.page_shift, a.c.pages, a.status);
       if (page_n < 0) return;
       const int64_t i = static_cast<int64_t>(page_n) * a.c.heads + h;
       ks_n = __ldg(a.c.ks + i);
@@ -347,14 +351,18 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
     };
     const auto load_tile = [&](int x, int win, int slot) {  // win: first tile of the window being computed
       if (x < x1) {
-        const int page = x < win + 32 ? __shfl_sync(0xFFFFFFFFu, page_c, x - win) : __shfl_sync(0xFFFFFFFFu, page_n, x - win - 32);
-        if (page >= 0) {
-          const uint32_t dst = smem_addr(ring + slot * C::kStage);
-          const int in_page = (walk.tile(x) * kTile) & (a.c.page - 1);
+        const bool next = x >= win + 16;
+        const int key0 = walk.tile(x) * kTile, y = 2 * (x - win) & 31;
+        const uint32_t dst = smem_addr(ring + slot * C::kStage);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {  // a granule's rows are one run of kGran * D bytes
+          const int page = __shfl_sync(0xFFFFFFFFu, next ? page_n : page_c, y + z);
+          if (page < 0) continue;
+          const int in_page = (key0 + z * kGran) & (a.c.page - 1);
           const int64_t src = (((static_cast<int64_t>(page) * a.c.heads + h) << a.c.page_shift) + in_page) * D + 16 * lane;
 #pragma unroll
-          for (int i = 0; i < C::kChunks / 2; ++i) {  // the tile's rows are one run of kTile * D bytes
-            const int idx = i * 32 + lane, r = idx / C::kChunks, c = idx % C::kChunks;
+          for (int i = 0; i < C::kChunks / 2; ++i) {
+            const int idx = i * 32 + lane, r = z * kGran + idx / C::kChunks, c = idx % C::kChunks;
             cp_async16(dst + stage_off<D>(r, c), a.c.k + src + 512 * i);
             cp_async16(dst + kTile * C::kPitch + stage_off<D>(r, c), a.c.v + src + 512 * i);
           }
@@ -365,9 +373,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
 
     fetch(x0);
     page_c = page_n, ks_c = ks_n, vs_c = vs_n;
-#pragma unroll
-    for (int i = 0; i < ST - 1; ++i) load_tile(x0 + i, x0, i);
-    fetch(x0 + 32);
+    load_tile(x0, x0, 0);
+    fetch(x0 + 16);
 
     // the query rows as the narrow operand of the scores, scaled into fp16's range, and as columns of S^T
     float slope[NT][2], mul[NT][2];
@@ -412,83 +419,96 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
         for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.0f;
     }
 
-    const auto compute_tile = [&](int x, int slot, float k_scale, float v_log) {
+    float fv[NT][2], fv_log = NAN;  // 2^(m + log2 vs - mv) for log2 vs = fv_log
+    const auto compute_tile = [&](int x, int slot, const float (&k_scale)[2], const float (&v_log)[2]) {
       const uint8_t *ks = ring + slot * C::kStage, *vs = ks + kTile * C::kPitch;
       const int key0 = walk.tile(x) * kTile;
-      float s[NT][4];
+      float s[2][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int z = 0; z < 2; ++z) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
-      {
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[z][nt][e] = 0.0f;
         uint32_t w0[KS], w1[KS];
-        load_k_words<D>(ks, g, t, w0);
-        load_k_words<D>(ks, g + 8, t, w1);
+        load_k_words<D>(ks, z * kGran + g, t, w0);
+        load_k_words<D>(ks, z * kGran + g + 8, t, w1);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           uint32_t a0, a1, a2, a3;
           codes_to_f16(w0[k], a0, a2);
           codes_to_f16(w1[k], a1, a3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
+          for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[z][nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[z][nt][e] *= k_scale[z] * mul[nt][e & 1];
       }
-      // scores, in units of log2; element e of s[nt]: key g + 8 (e >> 1), row 2 t + (e & 1)
-      const bool whole = key0 + kTile - 1 <= pos_min && (a.window == 0 || key0 > pos_max - a.window) && k_scale != -1.0f;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] *= k_scale * mul[nt][e & 1];
+      // scores, in units of log2; element e of s[z][nt]: key 16 z + g + 8 (e >> 1), row 2 t + (e & 1)
+      const bool whole = key0 + kTile - 1 <= pos_min && (a.window == 0 || key0 > pos_max - a.window) &&
+                         k_scale[0] != -1.0f && k_scale[1] != -1.0f;
       if (cap) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int z = 0; z < 2; ++z)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[nt][e] = cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(s[nt][e] * (2.0f * kLog2e)));
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              s[z][nt][e] = cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(s[z][nt][e] * (2.0f * kLog2e)));
       }
       if (a.slopes || !whole) {
-        bool any = whole;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int z = 0; z < 2; ++z)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = key0 + g + 8 * (e >> 1), at_q = pos[nt][e & 1];
-            float v = s[nt][e] + slope[nt][e & 1] * static_cast<float>(j - at_q);
-            if (!whole) {
-              const bool seen = k_scale != -1.0f && j < seq.n && at_q >= 0 &&
-                                ((j <= at_q && (a.window == 0 || at_q - j < a.window)) || j < prefix);
-              v = seen ? v : -INFINITY;
-              any = any || seen;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = key0 + z * kGran + g + 8 * (e >> 1), at_q = pos[nt][e & 1];
+              float v = s[z][nt][e] + slope[nt][e & 1] * static_cast<float>(j - at_q);
+              if (!whole) {
+                const bool seen = k_scale[z] != -1.0f && j < seq.n && at_q >= 0 &&
+                                  ((j <= at_q && (a.window == 0 || at_q - j < a.window)) || j < prefix);
+                v = seen ? v : -INFINITY;
+              }
+              s[z][nt][e] = v;
             }
-            s[nt][e] = v;
-          }
-        // a page of which no row sees anything may hold anything: it adds nothing
-        if (!__any_sync(0xFFFFFFFFu, any)) return;
       }
-      float top[NT][2];
       bool grew = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          top[nt][e] = fmaxf(s[nt][e], s[nt][e + 2]);
-          grew = grew || top[nt][e] > m[nt][e] + kRescale || top[nt][e] + v_log > mv[nt][e] + kRescale;
+          const float t0 = fmaxf(s[0][nt][e], s[0][nt][e + 2]), t1 = fmaxf(s[1][nt][e], s[1][nt][e + 2]);
+          grew = grew || fmaxf(t0, t1) > m[nt][e] + kRescale ||
+                 fmaxf(t0 + v_log[0], t1 + v_log[1]) > mv[nt][e] + kRescale;
         }
       if (__any_sync(0xFFFFFFFFu, grew)) {
+        fv_log = NAN;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float v = top[nt][e];
+            float v = -INFINITY, u = -INFINITY;
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+            for (int z = 0; z < 2; ++z) {
+              const float top = fmaxf(s[z][nt][e], s[z][nt][e + 2]);
+              v = fmaxf(v, top);
+              u = fmaxf(u, top == -INFINITY ? top : top + v_log[z]);  // (a page no row sees may have any scale)
+            }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+              u = fmaxf(u, __shfl_xor_sync(0xFFFFFFFFu, u, o));
+            }
             if (v > m[nt][e]) {
               l[nt][e] *= ex2(m[nt][e] - v);
               m[nt][e] = v;
             }
-            if (v + v_log > mv[nt][e]) {
-              const float al = ex2(mv[nt][e] - (v + v_log));
-              mv[nt][e] = v + v_log;
+            if (u > mv[nt][e]) {
+              const float al = ex2(mv[nt][e] - u);
+              mv[nt][e] = u;
 #pragma unroll
               for (int i = 0; i < MT; ++i) {
                 acc[i][nt][e] *= al;
@@ -497,60 +517,74 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NT>::kBlocks))
             }
           }
       }
-      uint32_t ph[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
+      for (int z = 0; z < 2; ++z) {
+        if (!(v_log[z] == fv_log)) {  // another page's scale, or new references
+          fv_log = v_log[z];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];  // a row that has seen no key yet
-          w[e] = ex2(s[nt][e] - ref);
-          l[nt][e & 1] += w[e];
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // (its exponent held in range: it is large only where 2^(s - m) is 0)
+              const float f = m[nt][e] + fv_log - mv[nt][e];
+              fv[nt][e] = mv[nt][e] == -INFINITY ? 0.0f : ex2(f > 126.0f ? 126.0f : f);
+            }
         }
+        uint32_t ph[NT][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // from 2^(s - m) to w (its exponent held in range: it is large only
-          // where 2^(s - m) is 0); a weight of 0 stays one whatever the page's scale
-          const float x = m[nt][e] + v_log - mv[nt][e];
-          const float fv = mv[nt][e] == -INFINITY ? 0.0f : ex2(x > 126.0f ? 126.0f : x);
-          w[e] = whole || w[e] > 0.0f ? w[e] * fv : 0.0f;
-          w[e + 2] = whole || w[e + 2] > 0.0f ? w[e + 2] * fv : 0.0f;
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float ref = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];  // a row that has seen no key yet
+            w[e] = ex2(s[z][nt][e] - ref);
+            l[nt][e & 1] += w[e];
+          }
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] *= fv[nt][e & 1];
+          } else {  // (a weight of 0 stays one whatever the scale of a page that the row does not see)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = w[e] > 0.0f ? w[e] * fv[nt][e & 1] : 0.0f;
+          }
+          ph[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+          ph[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
         }
-        ph[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
-        ph[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
-      }
-      uint32_t v0[D / 32], v1[D / 32], v2[D / 32], v3[D / 32];
-      load_v_words<D>(vs, 2 * t, g, v0);
-      load_v_words<D>(vs, 2 * t + 1, g, v1);
-      load_v_words<D>(vs, 2 * t + 8, g, v2);
-      load_v_words<D>(vs, 2 * t + 9, g, v3);
+        uint32_t v0[D / 32], v1[D / 32], v2[D / 32], v3[D / 32];
+        load_v_words<D>(vs, z * kGran + 2 * t, g, v0);
+        load_v_words<D>(vs, z * kGran + 2 * t + 1, g, v1);
+        load_v_words<D>(vs, z * kGran + 2 * t + 8, g, v2);
+        load_v_words<D>(vs, z * kGran + 2 * t + 9, g, v3);
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
+        for (int w = 0; w < D / 32; ++w) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t sel = half ? 0x7362u : 0x5140u;
-          uint32_t a0, a1, a2, a3;
-          codes_to_f16(__byte_perm(v0[w], v1[w], sel), a0, a1);
-          codes_to_f16(__byte_perm(v2[w], v3[w], sel), a2, a3);
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t sel = half ? 0x7362u : 0x5140u;
+            uint32_t a0, a1, a2, a3;
+            codes_to_f16(__byte_perm(v0[w], v1[w], sel), a0, a1);
+            codes_to_f16(__byte_perm(v2[w], v3[w], sel), a2, a3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[2 * w + half][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[2 * w + half][nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+          }
         }
       }
     };
 
-    int win = x0, slot = 0;
+    int win = x0;
 #pragma unroll 1
     for (int x = x0; x < x1; ++x) {
-      if (x == win + 32) {
+      if (x == win + 16) {
         win = x;
         page_c = page_n, ks_c = ks_n, vs_c = vs_n;
-        fetch(x + 32);
+        fetch(x + 16);
       }
-      cp_async_wait<ST - 2>();
+      const int slot = (x - x0) & 1, y = 2 * (x - win);
+      cp_async_wait<0>();
       __syncwarp();  // every lane's copies of this tile have landed, and all have read the slot loaded next
-      load_tile(x + ST - 1, win, slot == 0 ? ST - 1 : slot - 1);
-      compute_tile(x, slot, __shfl_sync(0xFFFFFFFFu, ks_c, x - win), __shfl_sync(0xFFFFFFFFu, vs_c, x - win));
-      slot = slot + 1 == ST ? 0 : slot + 1;
+      load_tile(x + 1, win, slot ^ 1);
+      const float ks2[2] = {__shfl_sync(0xFFFFFFFFu, ks_c, y), __shfl_sync(0xFFFFFFFFu, ks_c, y + 1)};
+      const float vs2[2] = {__shfl_sync(0xFFFFFFFFu, vs_c, y), __shfl_sync(0xFFFFFFFFu, vs_c, y + 1)};
+      compute_tile(x, slot, ks2, vs2);
     }
     cp_async_wait<0>();
     __syncwarp();
@@ -654,11 +688,11 @@ bool wide_rows(const KvAttnArgs &a) { return static_cast<int64_t>(a.s.max_q) * a
 
 template <int D, int NT>
 cudaError_t launch_t(const KvAttnArgs &a, float *partial, int num_sms, cudaStream_t s) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D>;
   cudaError_t e = ensure_kernel_smem<kv_decode_kernel<D, NT>>(static_cast<int>(C::kSmem), true);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(num_sms * C::kBlocks);
+  cfg.gridDim = dim3(num_sms * kBlocks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -692,7 +726,7 @@ bool kv_decode_fits(const KvAttnArgs &a) {  // all units in 31 bits
 
 size_t kv_decode_workspace_bytes(const KvAttnArgs &a, int num_sms) {
   // two parts a warp
-  const int64_t nt = wide_rows(a) ? 2 : 1, warps = static_cast<int64_t>(num_sms) * (nt == 2 ? 3 : 4) * kWarps;
+  const int64_t nt = wide_rows(a) ? 2 : 1, warps = static_cast<int64_t>(num_sms) * kBlocks * kWarps;
   return static_cast<size_t>(2 * warps * 8 * nt * (a.c.d + 4)) * sizeof(float);
 }
 
