@@ -507,3 +507,12 @@ def test_offsets_past_32_bits():
         assert_same(host(ko), wk, "k read back")
         assert_same(host(vo), wv, "v read back")
     assert status() == 0
+
+
+@pytest.mark.parametrize("B,hkv,G,ctx", [(2, 2, 4, 30000), (3, 40, 1, 4300), (40, 8, 2, 600), (9, 3, 8, 1500), (1, 1, 1, 70000)])
+def test_attention_single_tokens_at_the_ranges_of_the_cut(B, hkv, G, ctx):
+    """Few and many segments, short and long: pieces of warps and of blocks, against the 64-bit reference."""
+    rng = np.random.default_rng(ctx)
+    ctxs = [ctx] + [int(c) for c in rng.integers(0, ctx, B - 1)]
+    s, pages = R.make_seqs(rng, [1] * B, ctxs, 64)
+    check_attention(rng, s, R.random_cache(rng, pages, hkv, 64, 128), hkv * G)
