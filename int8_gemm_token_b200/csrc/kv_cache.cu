@@ -128,23 +128,37 @@ __device__ __forceinline__ void append_unit(const KvAppendArgs &a, const KvSeq &
   float *scale = (which ? a.c.vs : a.c.ks) + static_cast<int64_t>(page) * a.c.heads + h;
   const int old = lo & (a.c.page - 1);  // tokens that lie in the page already
   const float s_old = old > 0 ? *scale : 0.0f;
-  float x[PASSES][16];
+  // More than 2 passes hold their rows as bf16 and form the fp32 values twice,
+  // for the absmax and for the codes: 80 registers and 24 warps an SM, where
+  // holding the values takes 115 and 16 (a prompt of 8192 tokens, 8 heads and
+  // 32 query heads of 128: 39.1 us against 40.8; five prompts of up to 1531
+  // with pages of 16: 28.8 against 30.8). 1 or 2 passes keep them: a step of
+  // few tokens is bound by its latency (3.5 us; forming them again, 4.0).
+  const auto values = [&](int p, float(&x)[16]) {
+    const int pos = lo + p * TP + tok;
+    widen8(raw[p][0], x);
+    widen8(raw[p][1], x + 8);
+    if (16 * u < rot && tok < TP && pos < hi) {
+      float cs[8], sn[8];
+      const int64_t at = static_cast<int64_t>(pos) * (a.rot >> 1) + 8 * u;
+      load8f(a.cos + at, cs);
+      load8f(a.sin + at, sn);
+      rotate16(x, cs, sn, il);
+    }
+  };
+  constexpr bool kKeep = PASSES <= 2;
+  float x[kKeep ? PASSES : 1][16];
   float amax = 0.0f;
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
-    const int pos = lo + p * TP + tok;
-    widen8(raw[p][0], x[p]);
-    widen8(raw[p][1], x[p] + 8);
-    if (tok < TP && pos < hi) {
-      if (16 * u < rot) {
-        float cs[8], sn[8];
-        const int64_t at = static_cast<int64_t>(pos) * (a.rot >> 1) + 8 * u;
-        load8f(a.cos + at, cs);
-        load8f(a.sin + at, sn);
-        rotate16(x[p], cs, sn, il);
-      }
+    float(&y)[16] = x[kKeep ? p : 0];
+    values(p, y);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[p][i]));
+    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(y[i]));
+    if constexpr (!kKeep) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)  // the compiler is not to keep the values either
+        asm volatile("" : "+r"(raw[p][i].x), "+r"(raw[p][i].y), "+r"(raw[p][i].z), "+r"(raw[p][i].w));
     }
   }
 #pragma unroll
@@ -164,9 +178,11 @@ __device__ __forceinline__ void append_unit(const KvAppendArgs &a, const KvSeq &
   for (int p = 0; p < PASSES; ++p) {
     const int pos = lo + p * TP + tok;
     if (tok < TP && pos < hi) {
+      float(&y)[16] = x[kKeep ? p : 0];
+      if constexpr (!kKeep) values(p, y);
       int8_t *row = codes + (pos & (a.c.page - 1)) * D;
-      *reinterpret_cast<uint2 *>(row + 8 * c0) = codes8(x[p], r);
-      *reinterpret_cast<uint2 *>(row + 8 * c1) = codes8(x[p] + 8, r);
+      *reinterpret_cast<uint2 *>(row + 8 * c0) = codes8(y, r);
+      *reinterpret_cast<uint2 *>(row + 8 * c1) = codes8(y + 8, r);
     }
   }
   if (old > 0 && S != s_old) {
@@ -271,9 +287,10 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const __grid_const
 
 // Many new tokens: units [0, tiles * heads * 2) are a page of a head of k or
 // v each, for G threads (units whose page does not exist are skipped); the
-// warps that follow them have query rows.
+// warps that follow them have query rows. (24 warps an SM: at 20, pages of 16
+// lose 9 % and pages of 64 gain 1 %.)
 template <int D, int G>
-__global__ void __launch_bounds__(G > 32 ? G : kThreads)
+__global__ void __launch_bounds__(G > 32 ? G : kThreads, 768 / (G > 32 ? G : kThreads))
     append_pages_kernel(const __grid_constant__ KvAppendArgs a, int64_t tiles) {
   constexpr int BLOCK = G > 32 ? G : kThreads;
   __shared__ float s_red[BLOCK / 32];
