@@ -82,11 +82,26 @@ w8a8_status check_rows(const void *p, int64_t token_stride, int64_t head_stride,
   return W8A8_OK;
 }
 
-// Query rows of a kv head (new tokens x group) up to which the call takes the
-// kernel for few rows.
-constexpr int64_t kFewRows = 32;
+// Which kernel a call takes, by the query rows of a kv head (new tokens x
+// group): the one for few rows reads the codes of a context once for each 16 of
+// them; the other expands the context to bf16 once and costs nearly the same
+// for any number up to 256. Few : other, us a call, head dim 128, contexts of
+// 200, 1024, 4096, 16384:
+//   16 sequences x 8 kv heads, 32 rows 25 36 72 217 : 23 44 131 495
+//                              48 rows 29 44 99 320 : 24 44 132 494
+//                              64 rows 35 55 129 429 : 24 45 132 496
+//   8 sequences x 8 kv heads,  64 rows 24 34 69 216 : 22 32 88 289
+//   1 sequence x 32 kv heads,  64 rows 10 16 41 114 : 21 30 48 162
+//   1 sequence x 8 kv heads,   64 rows 9 16 22 40 : 17 28 26 46
+// so up to kFewRows always, and up to twice as many where (sequence, kv head)
+// pairs are few or contexts long.
+constexpr int64_t kFewRows = 32, kFewPairs = 64, kFewLong = 4096;
 
-bool few_rows(const KvAttnArgs &a) { return static_cast<int64_t>(a.s.max_q) * a.group <= kFewRows; }
+bool few_rows(const KvAttnArgs &a) {
+  const int64_t rows = static_cast<int64_t>(a.s.max_q) * a.group;
+  if (rows <= kFewRows) return true;
+  return rows <= 2 * kFewRows && (static_cast<int64_t>(a.s.batch) * a.c.heads <= kFewPairs || a.s.max_kv >= kFewLong);
+}
 
 // Cache, batch and heads of an attention call (what its workspace depends on).
 w8a8_status check_attention_shape(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch, int64_t tokens,

@@ -172,6 +172,13 @@ def gather(cache: Cache, table, first, start, keep):
     return outs
 
 
+def few_rows(max_new, hq, cache: Cache, s: Seqs):
+    """Whether the kernel for few query rows of a kv head takes the call (its products round to other formats)."""
+    heads, max_kv = cache.k.shape[1], s.table.shape[1] * cache.page
+    rows = int(max_new) * (hq // heads)
+    return rows <= 32 or (rows <= 64 and (len(s.kv) * heads <= 64 or max_kv >= 4096))
+
+
 def attention(cache: Cache, s: Seqs, q, scale, softcap=0.0, window=0, slopes=None, prefix=None, few=True):
     """(out, tolerance) float64 [tokens, q_heads, d], NaN in rows of no sequence.
 

@@ -169,7 +169,7 @@ def check_attention(rng, s, cache, hq, **kw):
     d, heads = cache.d, cache.k.shape[1]
     q = bf16_rows(rng, s.tokens, hq, d)
     scale = kw.pop("scale", d ** -0.5)
-    few = int(s.new.max()) * (hq // heads) <= 32
+    few = R.few_rows(s.new.max(), hq, cache, s)
     want, tol = R.attention(cache, s, synth.bits_to_f32(q), np.float32(scale), few=few,
                             slopes=kw.get("slopes"), prefix=kw.get("prefix"), softcap=kw.get("softcap", 0.0),
                             window=kw.get("window", 0))
@@ -249,6 +249,25 @@ def test_attention_few_long_blocks(d, page, hq, hkv, mask):
     rng = np.random.default_rng(d)
     s, pages = R.make_seqs(rng, [70, 40, 300], [5000, 3, 1500], page, spare=1)
     check_attention(rng, s, R.random_cache(rng, pages, hkv, page, d), hq, **mask_args(mask, hq))
+
+
+@pytest.mark.parametrize("mask", ["plain", "softcap", "window_33", "window_prefix", "all"])
+@pytest.mark.parametrize("new,ctx,hq,hkv", [
+    ([33, 1, 64], [100, 700, 0], 1, 1), ([11, 16, 2], [40, 0, 1200], 8, 2), ([1, 3, 2], [5, 900, 63], 21, 1),
+    ([40, 64, 7], [4100, 0, 33], 23, 23)])
+def test_attention_up_to_64_rows_of_a_head(new, ctx, hq, hkv, mask):
+    rng = np.random.default_rng(new[0] + hq)
+    s, pages = R.make_seqs(rng, new, ctx, 32, spare=1)
+    assert R.few_rows(max(new), hq, R.random_cache(rng, 1, hkv, 32, 64), s)
+    check_attention(rng, s, R.random_cache(rng, pages, hkv, 32, 64), hq, **mask_args(mask, hq))
+
+
+@pytest.mark.parametrize("hq,hkv,new", [(4, 4, 40), (8, 4, 31), (12, 4, 21)])
+def test_attention_up_to_64_rows_of_many_short_sequences(hq, hkv, new):
+    rng = np.random.default_rng(new)
+    s, pages = R.make_seqs(rng, [new, 1, 0, 17] * 5, [60, 0, 33, 200] * 5, 16, spare=1)
+    assert not R.few_rows(new, hq, R.random_cache(rng, 1, hkv, 16, 128), s)
+    check_attention(rng, s, R.random_cache(rng, pages, hkv, 16, 128), hq)
 
 
 @pytest.mark.parametrize("new,kv", [([1, 1, 1], [0, 5, 0]), ([3, 2], [1, 0]), ([50, 70, 40], [30, 70, 0])])
@@ -421,7 +440,7 @@ def test_layer_chain_from_projection_to_output_projection():
         nonlocal cache
         cache = R.append(cache, s, fx[:, hq:hq + hkv], fx[:, hq + hkv:], cos, sin)
         assert_cache(c, cache)
-        few = int(s.new.max()) * (hq // hkv) <= 32
+        few = R.few_rows(s.new.max(), hq, cache, s)
         want, tol = R.attention(cache, s, synth.bits_to_f32(host_bf16(q)), np.float32(d ** -0.5),
                                 few=few)
         return q, want, tol
@@ -496,7 +515,7 @@ def test_offsets_past_32_bits():
         assert_same(host(vs[at]), small.vs, "scales far in the cache")
         q = bf16_rows(rng, s.tokens, hq, d)
         out = W.w8a8_kv_attention(dev_bf16(q), c, batch_of(s))
-        few = max(new) <= 32
+        few = R.few_rows(max(new), hq, small, s_low)
         want, tol = R.attention(small, s_low, synth.bits_to_f32(q), np.float32(d ** -0.5), few=few)
         assert (np.abs(synth.bits_to_f32(host_bf16(out)) - want) <= tol).all()
         ko, vo = W.w8a8_kv_gather(c, dev(table), dev(np.zeros(2, np.int32)),
