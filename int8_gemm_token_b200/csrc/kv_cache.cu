@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(G > 32 ? G : kThreads, 768 / (G > 32 ? G : kTh
   if (seq.q == 0) return;
   const int start = max(seq.pos0(), 0);
   const int64_t pi = (start >> shift) + (tile - f(b));
-  if (start >= seq.n || pi > ((seq.n - 1) >> shift)) return;
+  // (where the starts descend, the search may end at a sequence whose slots lie behind this one)
+  if (tile < f(b) || start >= seq.n || pi > ((seq.n - 1) >> shift)) return;
   const int lo = max(start, static_cast<int>(pi) << shift);
   const int hi = min(seq.n, static_cast<int>((pi + 1) << shift));
   constexpr int TP = G / (D / 16), PASSES = (G / 2 + TP - 1) / TP;
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   if (!gather_ok(a, r0, r1, first)) return;
   const int64_t granule = first / kGran + (slot - f(b));
   const int end = first + (r1 - r0);  // one past the last position
-  if (granule * kGran >= end) return;
+  if (slot < f(b) || granule * kGran >= end) return;  // (as in append_pages_kernel)
   const int key0 = static_cast<int>(granule) * kGran;
   const int32_t page = load_page(a.table + b * a.table_ld, key0 >> a.c.page_shift, a.c.pages, a.status);
   const int64_t block = static_cast<int64_t>(max(page, 0)) * a.c.heads + h;

@@ -352,6 +352,28 @@ def test_bad_pages_and_sequences_are_reported_and_skipped():
     assert_cache(c, cache)
 
 
+def test_descending_starts_are_reported_and_stay_in_the_table():
+    """A search over starts that descend may end at a sequence whose pages lie behind: it takes none in front of its row."""
+    rng = np.random.default_rng(6)
+    start = np.array([0, 100, 110, 120, 5, 6, 200, 201], np.int32)
+    kv = np.array([100, 10, 10, 10, 1, 194, 1], np.int32)
+    batch, wide = len(kv), 16
+    # the call's table is the right half of a wider one, whose left half names a page of no sequence
+    table = np.full((batch, 2 * wide), batch * wide, np.int32)
+    table[:, wide:] = np.arange(batch * wide).reshape(batch, wide)
+    full = dev(table)
+    cache = R.random_cache(rng, batch * wide + 1, 2, 16, 64)
+    c = to_dev(cache)
+    x = dev_bf16(bf16_rows(rng, 201, 2, 64))
+    assert status() == 0
+    W.w8a8_kv_append(x, x, c, W.KVBatch(full[:, wide:], dev(start), dev(kv), 201))
+    assert status() == 12
+    for got, was in ((c.k_codes, cache.k), (c.v_codes, cache.v), (c.k_scale, cache.ks), (c.v_scale, cache.vs)):
+        assert_same(host(got)[-1], was[-1], "a page in front of the table's rows")
+    W.w8a8_kv_gather(to_dev(cache), full[:, wide:], dev(np.zeros(batch, np.int32)), dev(start), rows=201)
+    assert status() == 12
+
+
 def test_masked_pages_may_hold_anything():
     """Scales of infinity and NaN in pages that no row sees do not reach the output."""
     rng = np.random.default_rng(6)
