@@ -548,15 +548,19 @@ class KVBatch:
         if seq_start.device != page_table.device or kv_len.device != page_table.device:
             raise ValueError("expected page_table, seq_start and kv_len on one device")
         self.size, self._max_pages = batch, max_pages
-        self._c = _BatchStruct(page_table.data_ptr(), max(ld, max_pages), seq_start.data_ptr(), kv_len.data_ptr(),
-                               batch, max_pages, self.max_q_len, 0)
-        self._ref = ctypes.byref(self._c)
+        self._fields = (page_table.data_ptr(), max(ld, max_pages), seq_start.data_ptr(), kv_len.data_ptr(), batch,
+                        max_pages, self.max_q_len)
+        self._refs = {}
 
     def _for(self, cache: PagedKVCache):
-        """The C struct, with the longest length the table can hold where the caller gave none."""
-        most = self._max_pages * cache.page_size
-        self._c.max_kv_len = most if self.max_kv_len is None else int(self.max_kv_len)
-        return self._ref
+        """The C struct for caches of that page size, with the longest length
+        the table can hold where the caller gave none. (One for each page
+        size, never written again: threads and caches may share a batch.)"""
+        ref = self._refs.get(cache.page_size)
+        if ref is None:
+            most = self._max_pages * cache.page_size if self.max_kv_len is None else int(self.max_kv_len)
+            ref = self._refs[cache.page_size] = ctypes.byref(_BatchStruct(*self._fields, most))
+        return ref
 
 
 # These calls run once or more for every layer of a Decode step of a few

@@ -216,3 +216,22 @@ def test_reference_attention_against_a_plain_softmax():
     z = z.masked_fill(torch.arange(13)[None] > 9 + torch.arange(4)[:, None], float("-inf"))
     want = torch.einsum("hij,hjd->ihd", z.softmax(-1), v).numpy()
     assert np.allclose(out, want, rtol=1e-12, atol=1e-12) and (tol > 0).all()
+
+
+def test_a_batch_serves_caches_of_several_page_sizes():
+    """What one cache's call was given does not change when another's is prepared (two threads, one batch)."""
+    b = W.KVBatch(torch.zeros((3, 5), dtype=torch.int32), torch.zeros(4, dtype=torch.int32),
+                  torch.zeros(3, dtype=torch.int32), 1)
+    small, large = W.PagedKVCache.empty(6, 2, 16, 64, "cpu"), W.PagedKVCache.empty(6, 2, 128, 64, "cpu")
+    one, two = b._for(small), b._for(large)
+    assert one._obj.max_kv_len == 5 * 16 and two._obj.max_kv_len == 5 * 128
+    assert b._for(small)._obj.max_kv_len == 5 * 16 and one._obj.batch == two._obj.batch == 3
+
+
+def test_empty_cache():
+    c = W.PagedKVCache.empty(6, 2, 32, 96, "cpu")
+    assert c.k_codes.shape == c.v_codes.shape == (6, 2, 32, 96) and c.k_codes.dtype == torch.int8
+    assert c.k_scale.shape == c.v_scale.shape == (6, 2) and c.k_scale.dtype == torch.float32
+    assert not any(t.any() for t in (c.k_codes, c.v_codes, c.k_scale, c.v_scale))
+    with pytest.raises(ValueError):
+        W.PagedKVCache.empty(6, 2, 24, 96, "cpu")
