@@ -8,6 +8,7 @@ libw8a8.so is missing or cannot load, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -599,6 +600,12 @@ def _same_gpu(dev: int, *ts):
             raise ValueError(f"expected CUDA tensors on one device, got {sorted({str(t.device) for t in ts if t is not None})}")
 
 
+def _allocating(stream):
+    """Where what a call allocates is used on a given stream, it comes from that stream's memory: the
+    current stream may still use a freed block, or be given this one while the call runs."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 _entry = {}
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without making a Stream object
 
@@ -654,7 +661,8 @@ def w8a8_kv_append(k, v, cache: PagedKVCache, batch: KVBatch, cos=None, sin=None
     if q is not None:
         _, hq, qst, qsh = _heads3(q, None, d, "q", tokens)
         if q_out is None:
-            q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
+            with _allocating(stream):
+                q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
         else:
             _dense(q_out, torch.bfloat16, (tokens, hq, d), "q_out")
         qp, op = q.data_ptr(), q_out.data_ptr()
@@ -681,8 +689,9 @@ def w8a8_kv_gather(cache: PagedKVCache, page_table, first_pos, row_start, rows: 
         if rows is None:
             raise ValueError("rows: required where no output is given")
         shape = (int(rows), cache.kv_heads, cache.head_dim)
-        given = k_out = _out(None, out_dtype, shape, cache.device, (torch.bfloat16, torch.float32), "k_out")
-        v_out = torch.empty_like(k_out)
+        with _allocating(stream):
+            given = k_out = _out(None, out_dtype, shape, cache.device, (torch.bfloat16, torch.float32), "k_out")
+            v_out = torch.empty_like(k_out)
     else:
         what = "k_out" if k_out is not None else "v_out"
         if not isinstance(given, torch.Tensor) or given.dtype not in (torch.bfloat16, torch.float32) or given.dim() != 3:
@@ -719,14 +728,16 @@ def _attention(fn, q, cache, batch, scale, softcap, window, slopes, prefix_len, 
         _dense(prefix_len, torch.int32, (batch.size,), "prefix_len")
         pp = prefix_len.data_ptr()
     if out is None:
-        out = torch.empty((tokens, hq, d), dtype=out_dtype, device=q.device)
+        with _allocating(stream):
+            out = torch.empty((tokens, hq, d), dtype=out_dtype, device=q.device)
     else:
         _dense(out, out_dtype, (tokens, hq, d), "out")
     _same_gpu(dev, q, out, slopes, prefix_len, workspace, batch.page_table, *extra)
     if workspace is None:
         nbytes = w8a8_kv_attention_workspace_size(cache, batch, tokens, hq)
         if nbytes:
-            workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
+            with _allocating(stream):
+                workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
     else:
         workspace, nbytes = _workspace(0, q.device, workspace)
     sc = _ScoresStruct(d ** -0.5 if scale is None else scale, softcap, sp, window, pp)

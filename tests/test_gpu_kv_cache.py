@@ -511,6 +511,39 @@ def test_two_streams_at_once_equal_one_after_the_other():
         assert torch.equal(out, w[4])
 
 
+def test_what_a_call_allocates_belongs_to_the_given_stream():
+    """A workspace given back to the current stream could be written there while the call on the other one runs."""
+    rng = np.random.default_rng(12)
+    s, pages = R.make_seqs(rng, [300, 200], [500, 0], 16)
+    cache = R.random_cache(rng, pages, 2, 16, 64)
+    q = dev_bf16(bf16_rows(rng, s.tokens, 4, 64))
+    c, b = to_dev(cache), batch_of(s)
+    want = W.w8a8_kv_attention(q, c, b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    taken = set()
+    n = W.w8a8_kv_attention_workspace_size(c, b, s.tokens, 4)
+    for _ in range(3):
+        call = W._kv_call
+
+        def spy(fn, dev_, stream, *args):
+            taken.add(args[-2])  # (workspace, its bytes)
+            call(fn, dev_, stream, *args)
+
+        W._kv_call = spy
+        try:
+            out = W.w8a8_kv_attention(q, c, b, stream=side)
+        finally:
+            W._kv_call = call
+        taken.add(out.data_ptr())
+        mine = [torch.zeros((size,), dtype=torch.uint8, device="cuda") for size in (n, out.numel() * 2)]
+        assert not taken & {t.data_ptr() for t in mine}
+        side.synchronize()
+        assert torch.equal(out, want)
+        del out
+    assert status() == 0
+
+
 def test_offsets_past_32_bits():
     """Pages whose codes lie past 2^32 bytes of the cache."""
     page, hkv, hq, d = 128, 8, 8, 128
