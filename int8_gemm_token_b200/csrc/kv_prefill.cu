@@ -120,12 +120,14 @@ constexpr int kBins = 2048;
 constexpr int kMinShare = 4;
 
 __device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
-  __shared__ int32_t s_bin[kBins], s_sum[kExpandThreads], s_count[3];  // all tiles; split blocks; parts
+  __shared__ int32_t s_bin[kBins], s_sum[kExpandThreads], s_count[2];  // split blocks; parts
+  __shared__ unsigned long long s_all;                                 // tiles
   const int T = 2 * (kRows / a.group), tid = threadIdx.x;
   int shift = 0;
   while ((x.len / kKeys) >> shift >= kBins) ++shift;
   for (int i = tid; i < kBins; i += kExpandThreads) s_bin[i] = 0;
-  if (tid < 3) s_count[tid] = 0;
+  if (tid < 2) s_count[tid] = 0;
+  if (tid == 0) s_all = 0;
   __syncthreads();
   const auto block_of = [&](int32_t slot, QueryBlock &q) {
     int lo = 0, hi = a.s.batch;  // the last sequence whose slots begin at or before this one
@@ -157,13 +159,13 @@ __device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
   QueryBlock q;
   int share = INT32_MAX;
   if (x.most_parts > 0) {
-    int sum = 0;
+    unsigned long long sum = 0;
     for (int slot = tid; slot < x.slots; slot += kExpandThreads)
       if (block_of(slot, q)) sum += q.x1;
-    atomicAdd(&s_count[0], sum);
+    atomicAdd(&s_all, sum);
     __syncthreads();
-    const int64_t all = static_cast<int64_t>(s_count[0]) * a.c.heads;
-    share = max(kMinShare, static_cast<int>((all + x.sms - 1) / x.sms));
+    const int64_t all = static_cast<int64_t>(s_all) * a.c.heads;
+    share = static_cast<int>(min(int64_t(INT32_MAX / 2), max(int64_t(kMinShare), (all + x.sms - 1) / x.sms)));
   }
   // (a part more costs about 4 tiles and the join as much: not for a few tiles over the share)
   const auto parts_of = [&](int count) {
@@ -203,9 +205,9 @@ __device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
     if (block_of(slot, q)) {
       const int count = q.x1, parts = parts_of(count), per = (count + parts - 1) / parts;
       if (parts > 1) {
-        q.slot = atomicAdd(&s_count[2], parts);
+        q.slot = atomicAdd(&s_count[1], parts);
         q.parts = parts;
-        x.split[atomicAdd(&s_count[1], 1)] = q;
+        x.split[atomicAdd(&s_count[0], 1)] = q;
       }
       const int slot0 = q.slot;
       for (int i = 0; i < parts; ++i) {
@@ -216,7 +218,7 @@ __device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
       }
     }
   __syncthreads();
-  if (tid == 0) x.counters[2] = s_count[1];
+  if (tid == 0) x.counters[2] = s_count[0];
 }
 
 template <int D>
