@@ -145,8 +145,9 @@ w8a8_status w8a8_quant_per_tensor(const void *X, int64_t M, int64_t K, int64_t l
  * rounded to bf16 (RNE) for W8A8_BF16, or stored as fp32 for W8A8_FP32.
  * This is the read side of an INT8 KV cache kept in the Decode scheme: K and
  * V quantized once with w8a8_calibrate_static's S, r, Z and
- * w8a8_quant_per_tensor, and expanded by this call where attention needs
- * them (attention itself is not part of this library).
+ * w8a8_quant_per_tensor, and expanded by this call for an attention of the
+ * caller's (w8a8_kv_attention reads a paged cache with a scale for each page
+ * and head instead).
  * Source: PDMIX glossary §2.3 (q = round(x / S) + Z, so x ~ S (q - Z)) and
  * §3 (KVCache Quant, the companion of PDMIX); PDMIX configuration guide (the
  * W8A8C8 combination). No page fixes a separate scheme for the cache, so the
@@ -426,7 +427,7 @@ size_t int8_mixed_decomp_gemm_tc_workspace_size(int64_t M, int64_t N, int32_t ca
  * A cache holds `num_pages` pages of `page_size` tokens for each of
  * `kv_heads` heads; k and v alike:
  *   codes  int8 [num_pages, kv_heads, page_size, head_dim] dense, 16-byte aligned
- *   scale  fp32 [num_pages, kv_heads]; value = scale * (float) code
+ *   scale  fp32 [num_pages, kv_heads], not negative; value = scale * (float) code
  * page_size is 16, 32, 64 or 128; head_dim is 64, 96 or 128.
  *
  * A batch of sequences: sequence b's token at position p lies at slot
@@ -531,7 +532,8 @@ w8a8_status w8a8_kv_gather(const w8a8_kv_cache *cache, const int32_t *page_table
 /* What a score is before the softmax, and which keys a query sees. */
 typedef struct w8a8_kv_scores {
   float scale;               /* multiplies q . k; finite */
-  float softcap;             /* > 0: scores become softcap * tanh(score / softcap); 0: none */
+  float softcap;             /* > 0: scores become softcap * tanh(score / softcap), at most 4096 and with
+                                scale / softcap finite; 0: none */
   const float *slopes;       /* device fp32 [q_heads] or NULL: adds -slopes[h] * (distance of query and key) */
   int32_t window;            /* > 0: only keys less than `window` positions before the query; 0: no limit */
   const int32_t *prefix_len; /* device int32 [batch] or NULL: keys at positions below it are seen by every query */
@@ -548,9 +550,11 @@ typedef struct w8a8_kv_scores {
  * and sum and the accumulation are fp32. Rounding: the codes enter the tensor
  * cores exactly (an int8 code is exact in fp16 and in bf16) and so does q; the
  * page's scales are applied in fp32. The weights times v's scale are rounded
- * once for the second product: where max_q_len * (q_heads / kv_heads) <= 32 to
- * fp16 against the row's largest (2^-11 of the value, at least 2^-25 of the
- * largest), beyond to bf16 (2^-8 of the value).
+ * once for the second product, by the query rows of a kv head (max_q_len *
+ * (q_heads / kv_heads)): for up to 32, and up to 64 where batch * kv_heads <= 64
+ * or max_kv_len >= 4096, to fp16 against the row's largest (2^-11 of the value,
+ * at least 2^-25 of the largest); for more to bf16 (2^-8 of the value). A
+ * capped score is off by about softcap * 2^-22.
  *   q      device bf16 [tokens, q_heads, head_dim], strides in elements
  *          (multiples of 8, and not 0 where the axis has several elements)
  *   out    device bf16 [tokens, q_heads, head_dim] dense, 16-byte aligned

@@ -12,6 +12,7 @@ namespace {
 constexpr int64_t kMaxLen = int64_t(1) << 30;     // positions and packed rows stay far inside int32
 constexpr int32_t kMaxGroup = 128;                // query heads of a kv head
 constexpr int64_t kMaxBatch = 65535;
+constexpr float kMaxSoftcap = 4096.0f;
 
 bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
@@ -126,8 +127,9 @@ w8a8_status run_attention(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch
                           void *stream) {
   KvAttnArgs a;
   if (w8a8_status s = check_attention_shape(cache, batch, tokens, q_heads, &a)) return s;
-  if (!scores || !std::isfinite(scores->scale) || !std::isfinite(scores->softcap) || scores->softcap < 0.0f ||
-      scores->window < 0)
+  // (the capped form c - 2 c / (1 + 2^x) of c tanh in fp32 is off by c 2^-22 or so: kMaxSoftcap keeps that below 2^-10)
+  if (!scores || !std::isfinite(scores->scale) || !(scores->softcap >= 0.0f && scores->softcap <= kMaxSoftcap) ||
+      scores->window < 0 || (scores->softcap > 0.0f && !std::isfinite(scores->scale / scores->softcap)))
     return W8A8_ERR_INVALID_ARG;
   if (!aligned(scores->slopes, 4) || !aligned(scores->prefix_len, 4)) return W8A8_ERR_MISALIGNED;
   if (tokens == 0 || a.s.batch == 0 || a.s.max_q == 0) return W8A8_OK;
@@ -138,7 +140,7 @@ w8a8_status run_attention(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch
   a.scale = scores->scale;
   a.softcap = scores->softcap;
   a.slopes = scores->slopes;
-  a.window = scores->window;
+  a.window = scores->window < a.s.max_kv ? scores->window : 0;  // a window of all positions is none
   a.prefix = scores->prefix_len;
   a.out = out;
   a.r_out = r_out;

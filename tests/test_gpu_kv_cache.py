@@ -352,6 +352,35 @@ def test_bad_pages_and_sequences_are_reported_and_skipped():
     assert_cache(c, cache)
 
 
+@pytest.mark.parametrize("new", [(1, 1, 1), (70, 33, 129)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 100, 600])
+def test_a_window_of_all_positions_is_none(new, window):
+    rng = np.random.default_rng(3)
+    s, pages = R.make_seqs(rng, list(new), [400, 0, 15], 32, kv=[400 + new[0], 0, 15 + new[2]])
+    check_attention(rng, s, R.random_cache(rng, pages, 2, 32, 64), 4, window=window, prefix=np.array([30, 5, 0], np.int32))
+
+
+@pytest.mark.parametrize("most", [20, 201])
+def test_attention_reports_descending_starts(most):
+    """Every sequence is checked by itself; those that hold may have been served."""
+    rng = np.random.default_rng(8)
+    start = np.array([0, 20, 40, 60, 5, 6, 26, 27], np.int32)
+    kv = np.array([100, 10, 10, 10, 1, 20, 1], np.int32)
+    table = np.arange(7 * 16, dtype=np.int32).reshape(7, 16)
+    c = to_dev(R.random_cache(rng, 7 * 16, 2, 16, 64))
+    assert status() == 0
+    W.w8a8_kv_attention(dev_bf16(bf16_rows(rng, 60, 8, 64)), c, W.KVBatch(dev(table), dev(start), dev(kv), most))
+    assert status() == 12
+
+
+@pytest.mark.parametrize("new,ctx", [([1, 1], [100, 2]), ([3, 130], [1, 40])])
+@pytest.mark.parametrize("d,hq", [(64, 128), (128, 128), (96, 65), (128, 43)])
+def test_attention_large_groups(d, hq, new, ctx):
+    rng = np.random.default_rng(hq)
+    s, pages = R.make_seqs(rng, new, ctx, 64, spare=1)
+    check_attention(rng, s, R.random_cache(rng, pages, 1, 64, d), hq)
+
+
 def test_descending_starts_are_reported_and_stay_in_the_table():
     """A search over starts that descend may end at a sequence whose pages lie behind: it takes none in front of its row."""
     rng = np.random.default_rng(6)

@@ -101,6 +101,14 @@ def test_attention_refusals():
     assert f(cache(), batch(), 3, P, 512, 128, 4, s, P, P + 2, P, P, 1 << 40, None) == 2
 
 
+def test_attention_refuses_caps_that_fp32_does_not_hold():
+    for bad in ((1.0, 5000.0, None, 0, None), (1.0, float("inf"), None, 0, None), (1.0, 1e-39, None, 0, None),
+                (1e30, 1e-10, None, 0, None)):
+        assert attention(scores=bad) == 1
+    for good in ((1.0, 4096.0, None, 0, None), (1.0, 1e-30, None, 0, None), (0.0, 1e-39, None, 0, None)):
+        assert attention(tokens=0, scores=good) == 0
+
+
 def test_gather_refusals():
     assert gather(dt=2) == 4
     assert gather(rows=-1) == 1 and gather(rows=(1 << 30) + 1) == 3
