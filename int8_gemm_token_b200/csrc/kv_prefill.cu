@@ -610,285 +610,288 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t steps = 0, outs = 0;  // score tiles and outputs of this query tile so far
     Item item;
     for (int it = 0; take(it, item, ok); ++it) {
-    const int toks = toks_of(item.q, w), count = count_of(item.q, w), n = item.q.n, prefix = item.q.prefix, x0 = item.q.x0;
-    const int slot = item.q.slot < 0 ? -1 : item.q.slot * a.c.heads + item.h;
-    const TileWalk walk = walk_of(item.q);
-    const int row0 = item.q.row + w * tpt, h0 = item.h * a.group;
-    const int pos_min = item.q.pos + w * tpt, pos_max = pos_min + toks - 1;
-    const int64_t krow = (static_cast<int64_t>(item.q.b) * a.c.heads + item.h) * x.len;
-    done_with(it);
-    const bool real = tok < toks;
-    const int pos = real ? pos_min + tok : -1;
-    const float slope = a.slopes && real ? __ldg(a.slopes + h0 + row - tok * a.group) * kLog2e : 0.0f;
-    float m = -INFINITY, l = 0.0f;
-    const float *ks = x.ks + krow / kGran, *vs = x.vs + krow / kGran;
-    for (int j = 0; j < count; ++j) {
-      const int key0 = walk.tile(x0 + j) * kKeys;
-      float kc[8], vc[8];  // scales of the tile's granules
+      const int toks = toks_of(item.q, w), count = count_of(item.q, w);
+      const int n = item.q.n, prefix = item.q.prefix, x0 = item.q.x0;
+      const int slot = item.q.slot < 0 ? -1 : item.q.slot * a.c.heads + item.h;
+      const TileWalk walk = walk_of(item.q);
+      const int row0 = item.q.row + w * tpt, h0 = item.h * a.group;
+      const int pos_min = item.q.pos + w * tpt, pos_max = pos_min + toks - 1;
+      const int64_t krow = (static_cast<int64_t>(item.q.b) * a.c.heads + item.h) * x.len;
+      done_with(it);
+      const bool real = tok < toks;
+      const int pos = real ? pos_min + tok : -1;
+      const float slope = a.slopes && real ? __ldg(a.slopes + h0 + row - tok * a.group) * kLog2e : 0.0f;
+      float m = -INFINITY, l = 0.0f;
+      const float *ks = x.ks + krow / kGran, *vs = x.vs + krow / kGran;
+      for (int j = 0; j < count; ++j) {
+        const int key0 = walk.tile(x0 + j) * kKeys;
+        float kc[8], vc[8];  // scales of the tile's granules
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float4 k4 = *reinterpret_cast<const float4 *>(ks + key0 / kGran + 4 * e);
-        const float4 v4 = *reinterpret_cast<const float4 *>(vs + key0 / kGran + 4 * e);
-        kc[4 * e] = k4.x, kc[4 * e + 1] = k4.y, kc[4 * e + 2] = k4.z, kc[4 * e + 3] = k4.w;
-        vc[4 * e] = v4.x, vc[4 * e + 1] = v4.y, vc[4 * e + 2] = v4.z, vc[4 * e + 3] = v4.w;
-      }
-      bool whole = key0 + kKeys - 1 <= pos_min && (a.window == 0 || key0 > pos_max - a.window);
+        for (int e = 0; e < 2; ++e) {
+          const float4 k4 = *reinterpret_cast<const float4 *>(ks + key0 / kGran + 4 * e);
+          const float4 v4 = *reinterpret_cast<const float4 *>(vs + key0 / kGran + 4 * e);
+          kc[4 * e] = k4.x, kc[4 * e + 1] = k4.y, kc[4 * e + 2] = k4.z, kc[4 * e + 3] = k4.w;
+          vc[4 * e] = v4.x, vc[4 * e + 1] = v4.y, vc[4 * e + 2] = v4.z, vc[4 * e + 3] = v4.w;
+        }
+        bool whole = key0 + kKeys - 1 <= pos_min && (a.window == 0 || key0 > pos_max - a.window);
 #pragma unroll
-      for (int g = 0; g < 8; ++g) whole = whole && kc[g] != -1.0f;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&s_bar[w], (steps + static_cast<uint32_t>(j)) & 1u, abort_flag, limit_ns))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      // the row's scores, all of them in flight at once
-      uint32_t s0[32], s1[32], s2[32], s3[32];
-      tmem_ld_32x32b_x32(t_s, s0);
-      tmem_ld_32x32b_x32(t_s + 32, s1);
-      tmem_ld_32x32b_x32(t_s + 64, s2);
-      tmem_ld_32x32b_x32(t_s + 96, s3);
-      tmem_ld_wait();
-      float top = -INFINITY;
-      if (whole && plain) {
-        const auto largest = [&](const uint32_t(&s)[32], int c) {
+        for (int g = 0; g < 8; ++g) whole = whole && kc[g] != -1.0f;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&s_bar[w], (steps + static_cast<uint32_t>(j)) & 1u, abort_flag,
+                                                       limit_ns))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // the row's scores, all of them in flight at once
+        uint32_t s0[32], s1[32], s2[32], s3[32];
+        tmem_ld_32x32b_x32(t_s, s0);
+        tmem_ld_32x32b_x32(t_s + 32, s1);
+        tmem_ld_32x32b_x32(t_s + 64, s2);
+        tmem_ld_32x32b_x32(t_s + 96, s3);
+        tmem_ld_wait();
+        float top = -INFINITY;
+        if (whole && plain) {
+          const auto largest = [&](const uint32_t(&s)[32], int c) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            float v = __uint_as_float(s[16 * g]), u = __uint_as_float(s[16 * g + 1]);
+            for (int g = 0; g < 2; ++g) {
+              float v = __uint_as_float(s[16 * g]), u = __uint_as_float(s[16 * g + 1]);
 #pragma unroll
-            for (int e = 2; e < 16; e += 4) {
-              v = max3(v, __uint_as_float(s[16 * g + e]), __uint_as_float(s[16 * g + e + 1]));
-              if (e + 2 < 16) u = max3(u, __uint_as_float(s[16 * g + e + 2]), __uint_as_float(s[16 * g + e + 3]));
+              for (int e = 2; e < 16; e += 4) {
+                v = max3(v, __uint_as_float(s[16 * g + e]), __uint_as_float(s[16 * g + e + 1]));
+                if (e + 2 < 16) u = max3(u, __uint_as_float(s[16 * g + e + 2]), __uint_as_float(s[16 * g + e + 3]));
+              }
+              kc[2 * c + g] *= mul;
+              top = fmaxf(top, fmaxf(v, u) * kc[2 * c + g]);
             }
-            kc[2 * c + g] *= mul;
-            top = fmaxf(top, fmaxf(v, u) * kc[2 * c + g]);
-          }
-        };
-        largest(s0, 0);
-        largest(s1, 1);
-        largest(s2, 2);
-        largest(s3, 3);
-      } else {  // element by element
-        const float far = slope * static_cast<float>(key0 - pos);
-        // keys key0 + e of this row: e <= hi and e >= lo, or e < pre
-        const int hi = pos < 0 ? -1 : min(pos, n - 1) - key0;
-        const int lo = a.window > 0 ? pos - a.window + 1 - key0 : -key0;
-        const int pre = pos < 0 ? 0 : min(prefix, n) - key0;
-        // CAP: tanh cap; BIAS: distance bias; MASK: some row of the tile does
-        // not see some key (CAP decides about the other two as it goes)
-        const auto finish = [&](auto cap_c, auto bias_c, auto mask_c, uint32_t(&s)[32], int c) {
-          constexpr bool CAP = decltype(cap_c)::value, BIAS = decltype(bias_c)::value, MASK = decltype(mask_c)::value;
+          };
+          largest(s0, 0);
+          largest(s1, 1);
+          largest(s2, 2);
+          largest(s3, 3);
+        } else {  // element by element
+          const float far = slope * static_cast<float>(key0 - pos);
+          // keys key0 + e of this row: e <= hi and e >= lo, or e < pre
+          const int hi = pos < 0 ? -1 : min(pos, n - 1) - key0;
+          const int lo = a.window > 0 ? pos - a.window + 1 - key0 : -key0;
+          const int pre = pos < 0 ? 0 : min(prefix, n) - key0;
+          // CAP: tanh cap; BIAS: distance bias; MASK: some row of the tile does
+          // not see some key (CAP decides about the other two as it goes)
+          const auto finish = [&](auto cap_c, auto bias_c, auto mask_c, uint32_t(&s)[32], int c) {
+            constexpr bool CAP = decltype(cap_c)::value, BIAS = decltype(bias_c)::value, MASK = decltype(mask_c)::value;
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float k1 = kc[2 * c + g], f = k1 * mul;
-            const int e0 = 32 * c + 16 * g;
+            for (int g = 0; g < 2; ++g) {
+              const float k1 = kc[2 * c + g], f = k1 * mul;
+              const int e0 = 32 * c + 16 * g;
+              float y[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(s[16 * g + i]);
+              if constexpr (CAP) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  y[i] = cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(y[i] * (f * (2.0f * kLog2e))));
+              }
+              if constexpr (BIAS) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                  float b0 = fmaf(slope, static_cast<float>(e0 + i), far);
+                  float b1 = fmaf(slope, static_cast<float>(e0 + i + 1), far);
+                  axpy2(b0, b1, y[i], y[i + 1], CAP ? 1.0f : f);
+                  y[i] = b0, y[i + 1] = b1;
+                }
+              } else if constexpr (!CAP) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) mul_f32x2(y[i], y[i + 1], f, y[i], y[i + 1]);
+              }
+              if constexpr (MASK) {
+                // bits of the granule's keys that this row sees
+                uint32_t seen = (bits_below(hi + 1 - e0) & ~bits_below(lo - e0)) | bits_below(pre - e0);
+                if (k1 == -1.0f) seen = 0;
+                // a page of which this row sees nothing may hold anything: its weights are 0 times 0
+                if (seen == 0) vc[2 * c + g] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = (seen >> i) & 1u ? y[i] : -INFINITY;
+              }
+              float v = y[0], u = y[1];
+#pragma unroll
+              for (int i = 2; i < 16; i += 4) {
+                v = max3(v, y[i], y[i + 1]);
+                if (i + 2 < 16) u = max3(u, y[i + 2], y[i + 3]);
+              }
+              top = max3(top, v, u);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) s[16 * g + i] = __float_as_uint(y[i]);
+              kc[2 * c + g] = 1.0f;
+            }
+          };
+          const auto finish_row = [&](auto cap_c, auto bias_c, auto mask_c) {
+            finish(cap_c, bias_c, mask_c, s0, 0);
+            finish(cap_c, bias_c, mask_c, s1, 1);
+            finish(cap_c, bias_c, mask_c, s2, 2);
+            finish(cap_c, bias_c, mask_c, s3, 3);
+          };
+          if (cap)
+            finish_row(Yes(), Yes(), Yes());
+          else if (a.slopes && whole)
+            finish_row(No(), Yes(), No());
+          else if (a.slopes)
+            finish_row(No(), Yes(), Yes());
+          else
+            finish_row(No(), No(), Yes());
+        }
+        const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float fr = grow ? ex2(m - top) : 1.0f;
+          if (grow) m = top;
+          l *= fr;
+          if (j > 0) {  // O_w(j - 1) is complete, O_w(j) waits for this warp
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(t_o + 16 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fr);
+              tmem_st_32x32b_x16(t_o + 16 * c, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.0f : -m;
+        float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
+        // 32 weights, packed by two; stage by stage over a granule, so that the
+        // steps of 16 independent elements overlap
+        uint32_t p[32];
+        const auto weights = [&](const uint32_t(&s)[32], int c) {
+#pragma unroll
+          for (int h2 = 0; h2 < 2; ++h2) {
+            const int g = 2 * c + h2;
             float y[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(s[16 * g + i]);
-            if constexpr (CAP) {
+            for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(s[16 * h2 + e]);
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                y[i] = cap2 - __fdividef(2.0f * cap2, 1.0f + ex2(y[i] * (f * (2.0f * kLog2e))));
+            for (int e = 0; e < 16; e += 2) fma2(y[e], y[e + 1], kc[g], ref);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = ex2(y[e]);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              add2(l0, l1, y[e], y[e + 1]);
+              add2(l2, l3, y[e + 2], y[e + 3]);
             }
-            if constexpr (BIAS) {
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                float b0 = fmaf(slope, static_cast<float>(e0 + i), far), b1 = fmaf(slope, static_cast<float>(e0 + i + 1), far);
-                axpy2(b0, b1, y[i], y[i + 1], CAP ? 1.0f : f);
-                y[i] = b0, y[i + 1] = b1;
-              }
-            } else if constexpr (!CAP) {
+            for (int e = 0; e < 16; e += 2) mul_f32x2(y[e], y[e + 1], vc[g], y[e], y[e + 1]);
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) mul_f32x2(y[i], y[i + 1], f, y[i], y[i + 1]);
-            }
-            if constexpr (MASK) {
-              // bits of the granule's keys that this row sees
-              uint32_t seen = (bits_below(hi + 1 - e0) & ~bits_below(lo - e0)) | bits_below(pre - e0);
-              if (k1 == -1.0f) seen = 0;
-              // a page of which this row sees nothing may hold anything: its weights are 0 times 0
-              if (seen == 0) vc[2 * c + g] = 0.0f;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = (seen >> i) & 1u ? y[i] : -INFINITY;
-            }
-            float v = y[0], u = y[1];
-#pragma unroll
-            for (int i = 2; i < 16; i += 4) {
-              v = max3(v, y[i], y[i + 1]);
-              if (i + 2 < 16) u = max3(u, y[i + 2], y[i + 3]);
-            }
-            top = max3(top, v, u);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[16 * g + i] = __float_as_uint(y[i]);
-            kc[2 * c + g] = 1.0f;
+            for (int e = 0; e < 16; e += 2) p[16 * (c & 1) + 8 * h2 + (e >> 1)] = pack_bf16x2(y[e], y[e + 1]);
           }
         };
-        const auto finish_row = [&](auto cap_c, auto bias_c, auto mask_c) {
-          finish(cap_c, bias_c, mask_c, s0, 0);
-          finish(cap_c, bias_c, mask_c, s1, 1);
-          finish(cap_c, bias_c, mask_c, s2, 2);
-          finish(cap_c, bias_c, mask_c, s3, 3);
+        const auto hand_over = [&](int half) {  // the weights of 64 keys, over scores that have been read
+          tmem_st_32x32b_x32(t_s + 32 * half, p);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_bar[2 * w + half]);
         };
-        if (cap)
-          finish_row(Yes(), Yes(), Yes());
-        else if (a.slopes && whole)
-          finish_row(No(), Yes(), No());
-        else if (a.slopes)
-          finish_row(No(), Yes(), Yes());
-        else
-          finish_row(No(), No(), Yes());
+        weights(s0, 0);
+        weights(s1, 1);
+        hand_over(0);
+        weights(s2, 2);
+        weights(s3, 3);
+        hand_over(1);
+        l += (l0 + l1) + (l2 + l3);
       }
-      const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
-      if (__any_sync(0xFFFFFFFFu, grow)) {
-        const float fr = grow ? ex2(m - top) : 1.0f;
-        if (grow) m = top;
-        l *= fr;
-        if (j > 0) {  // O_w(j - 1) is complete, O_w(j) waits for this warp
+      if (ok && count > 0)
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&o_bar[w], outs & 1u, abort_flag, limit_ns));
+      if (!ok) break;
+      tc_fence_after();
+      if (slot >= 0) {  // a part: its sums, maximum and sum of weights
+        float *const part = x.parts + static_cast<int64_t>(slot) * part_floats<D>();
+        *reinterpret_cast<float2 *>(part + 2 * kRows * D + (w * kRows + row) * 2) = make_float2(count > 0 ? m : -INFINITY, l);
+        if (count > 0) {
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             uint32_t o[16];
             tmem_ld_32x32b_x16(t_o + 16 * c, o);
             tmem_ld_wait();
+            // dims by 4, rows side by side: a warp's stores are runs of 512 bytes
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fr);
-            tmem_st_32x32b_x16(t_o + 16 * c, o);
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4 *>(part + (static_cast<int64_t>(w * (D / 4) + 4 * c + e) * kRows + row) * 4) =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
-      }
-      const float ref = m == -INFINITY ? 0.0f : -m;
-      float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
-      // 32 weights, packed by two; stage by stage over a granule, so that the
-      // steps of 16 independent elements overlap
-      uint32_t p[32];
-      const auto weights = [&](const uint32_t(&s)[32], int c) {
-#pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          const int g = 2 * c + h2;
-          float y[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(s[16 * h2 + e]);
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) fma2(y[e], y[e + 1], kc[g], ref);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = ex2(y[e]);
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            add2(l0, l1, y[e], y[e + 1]);
-            add2(l2, l3, y[e + 2], y[e + 3]);
-          }
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) mul_f32x2(y[e], y[e + 1], vc[g], y[e], y[e + 1]);
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) p[16 * (c & 1) + 8 * h2 + (e >> 1)] = pack_bf16x2(y[e], y[e + 1]);
-        }
-      };
-      const auto hand_over = [&](int half) {  // the weights of 64 keys, over scores that have been read
-        tmem_st_32x32b_x32(t_s + 32 * half, p);
-        tmem_st_wait();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_bar[2 * w + half]);
-      };
-      weights(s0, 0);
-      weights(s1, 1);
-      hand_over(0);
-      weights(s2, 2);
-      weights(s3, 3);
-      hand_over(1);
-      l += (l0 + l1) + (l2 + l3);
-    }
-    if (ok && count > 0)
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&o_bar[w], outs & 1u, abort_flag, limit_ns));
-    if (!ok) break;
-    tc_fence_after();
-    if (slot >= 0) {  // a part: its sums, maximum and sum of weights
-      float *const part = x.parts + static_cast<int64_t>(slot) * part_floats<D>();
-      *reinterpret_cast<float2 *>(part + 2 * kRows * D + (w * kRows + row) * 2) = make_float2(count > 0 ? m : -INFINITY, l);
-      if (count > 0) {
-#pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t o[16];
-          tmem_ld_32x32b_x16(t_o + 16 * c, o);
-          tmem_ld_wait();
-          // dims by 4, rows side by side: a warp's stores are runs of 512 bytes
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4 *>(part + (static_cast<int64_t>(w * (D / 4) + 4 * c + e) * kRows + row) * 4) =
-                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        }
-      }
-      tc_fence_before();
-      steps += static_cast<uint32_t>(count);
-      outs += count > 0 ? 1u : 0u;
-      continue;
-    }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const float r_out = a.r_out ? __ldg(a.r_out) : 0.0f;
-    const int z_out = a.r_out ? __ldg(a.z_out) : 0;
-    // 64 dims of the warp's 32 rows at a time through its staging (swizzled as
-    // TMA would). bf16 rows of whole tokens that are all the item's leave as
-    // one tensor store, which the warp does not wait for; others by
-    // neighbouring lanes.
-    const bool tensor_store = !a.r_out && 32 % a.group == 0 && (warp & 3) * 32 + 32 <= toks * a.group;
-#pragma unroll
-    for (int part = 0; part < C::kAtoms; ++part) {
-      constexpr int kMost = 64;
-      const int dims = D - kMost * part < kMost ? D - kMost * part : kMost;
-      uint32_t o4[kMost / 16][16];
-#pragma unroll
-      for (int c = 0; c < kMost / 16; ++c) {
-        if (16 * c >= dims) continue;
-        if (count > 0) {
-          tmem_ld_32x32b_x16(t_o + kMost * part + 16 * c, o4[c]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o4[c][e] = 0;
-        }
-      }
-      tmem_ld_wait();
-#pragma unroll
-      for (int c = 0; c < kMost / 16; ++c) {
-        if (16 * c >= dims) continue;
-        const uint32_t(&o)[16] = o4[c];
-        uint32_t y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          y[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-        uint8_t *const at = stage + lane * kStageRow;
-        if (c == 0) {  // the staging's last store has read it
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
-        }
-        *reinterpret_cast<uint4 *>(at + (((2 * c) ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<uint4 *>(at + (((2 * c + 1) ^ (lane & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-      }
-      if (tensor_store) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&tmOut, stage, kMost * part, h0, row0 + (warp & 3) * (32 / a.group));
-          bulk_commit_group();
-        }
+        steps += static_cast<uint32_t>(count);
+        outs += count > 0 ? 1u : 0u;
         continue;
       }
-      __syncwarp();
-      const int chunks = dims / 8;
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const float r_out = a.r_out ? __ldg(a.r_out) : 0.0f;
+      const int z_out = a.r_out ? __ldg(a.z_out) : 0;
+      // 64 dims of the warp's 32 rows at a time through its staging (swizzled as
+      // TMA would). bf16 rows of whole tokens that are all the item's leave as
+      // one tensor store, which the warp does not wait for; others by
+      // neighbouring lanes.
+      const bool tensor_store = !a.r_out && 32 % a.group == 0 && (warp & 3) * 32 + 32 <= toks * a.group;
 #pragma unroll
-      for (int k = 0; k < kMost / 8; ++k) {
-        if (k >= chunks) continue;
-        const int i = k * 32 + lane, r1 = i / chunks, c = i - r1 * chunks, r = (warp & 3) * 32 + r1;
-        const int r_tok = r / a.group;
-        if (r_tok >= toks) continue;
-        const uint4 v = *reinterpret_cast<const uint4 *>(stage + r1 * kStageRow + ((c ^ (r1 & 7)) << 4));
-        const int64_t elem =
-            (static_cast<int64_t>(row0 + r_tok) * a.q_heads + h0 + r - r_tok * a.group) * D + kMost * part + 8 * c;
-        if (!a.r_out)
-          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + elem) = v;
-        else
-          *reinterpret_cast<uint2 *>(static_cast<int8_t *>(a.out) + elem) = quant8_asym_sat(v, r_out, z_out);
+      for (int part = 0; part < C::kAtoms; ++part) {
+        constexpr int kMost = 64;
+        const int dims = D - kMost * part < kMost ? D - kMost * part : kMost;
+        uint32_t o4[kMost / 16][16];
+#pragma unroll
+        for (int c = 0; c < kMost / 16; ++c) {
+          if (16 * c >= dims) continue;
+          if (count > 0) {
+            tmem_ld_32x32b_x16(t_o + kMost * part + 16 * c, o4[c]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o4[c][e] = 0;
+          }
+        }
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < kMost / 16; ++c) {
+          if (16 * c >= dims) continue;
+          const uint32_t(&o)[16] = o4[c];
+          uint32_t y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            y[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          uint8_t *const at = stage + lane * kStageRow;
+          if (c == 0) {  // the staging's last store has read it
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+          }
+          *reinterpret_cast<uint4 *>(at + (((2 * c) ^ (lane & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4 *>(at + (((2 * c + 1) ^ (lane & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        if (tensor_store) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tmOut, stage, kMost * part, h0, row0 + (warp & 3) * (32 / a.group));
+            bulk_commit_group();
+          }
+          continue;
+        }
+        __syncwarp();
+        const int chunks = dims / 8;
+#pragma unroll
+        for (int k = 0; k < kMost / 8; ++k) {
+          if (k >= chunks) continue;
+          const int i = k * 32 + lane, r1 = i / chunks, c = i - r1 * chunks, r = (warp & 3) * 32 + r1;
+          const int r_tok = r / a.group;
+          if (r_tok >= toks) continue;
+          const uint4 v = *reinterpret_cast<const uint4 *>(stage + r1 * kStageRow + ((c ^ (r1 & 7)) << 4));
+          const int64_t elem =
+              (static_cast<int64_t>(row0 + r_tok) * a.q_heads + h0 + r - r_tok * a.group) * D + kMost * part + 8 * c;
+          if (!a.r_out)
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + elem) = v;
+          else
+            *reinterpret_cast<uint2 *>(static_cast<int8_t *>(a.out) + elem) = quant8_asym_sat(v, r_out, z_out);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-    }
-    tc_fence_before();  // O has been read before this warp's next weights let it be overwritten
-    steps += static_cast<uint32_t>(count);
-    outs += count > 0 ? 1u : 0u;
+      tc_fence_before();  // O has been read before this warp's next weights let it be overwritten
+      steps += static_cast<uint32_t>(count);
+      outs += count > 0 ? 1u : 0u;
     }
     if (lane == 0) bulk_wait_all();  // every store of this warp has completed before the block leaves
     __syncwarp();
