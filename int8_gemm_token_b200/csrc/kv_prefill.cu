@@ -117,7 +117,7 @@ struct Expanded {
 // at most that share. Parts of split blocks are at most twice the SMs: each
 // split block has more than a share, so ceil(count / share) < 2 count / share.
 constexpr int kBins = 2048;
-constexpr int kMinShare = 4;
+constexpr int kMinShare = 4, kMinOver = 8;
 
 __device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
   __shared__ int32_t s_bin[kBins], s_sum[kExpandThreads], s_count[2];  // split blocks; parts
@@ -156,12 +156,20 @@ __device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
     q.pad[0] = q.pad[1] = 0;
     return true;
   };
-  QueryBlock q;
+  // Each thread's first block is kept: where blocks may be split there are
+  // hardly more of them than threads, and the search is most of the work.
+  QueryBlock q0;
+  const bool has0 = tid < x.slots && block_of(tid, q0);
+  const auto each = [&](auto f) {
+    if (has0) f(q0);
+    QueryBlock q;
+    for (int slot = tid + kExpandThreads; slot < x.slots; slot += kExpandThreads)
+      if (block_of(slot, q)) f(q);
+  };
   int share = INT32_MAX;
   if (x.most_parts > 0) {
     unsigned long long sum = 0;
-    for (int slot = tid; slot < x.slots; slot += kExpandThreads)
-      if (block_of(slot, q)) sum += q.x1;
+    each([&](const QueryBlock &q) { sum += q.x1; });
     atomicAdd(&s_all, sum);
     __syncthreads();
     const int64_t all = static_cast<int64_t>(s_all) * a.c.heads;
@@ -169,14 +177,13 @@ __device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
   }
   // (a part more costs about 4 tiles and the join as much: not for a few tiles over the share)
   const auto parts_of = [&](int count) {
-    return share < INT32_MAX && count > share + max(8, share / 2) ? (count + share - 1) / share : 1;
+    return share < INT32_MAX && count > share + max(kMinOver, share / 2) ? (count + share - 1) / share : 1;
   };
   const auto bin_of = [&](int tiles) { return kBins - 1 - min(tiles >> shift, kBins - 1); };
-  for (int slot = tid; slot < x.slots; slot += kExpandThreads)
-    if (block_of(slot, q)) {
-      const int parts = parts_of(q.x1), per = (q.x1 + parts - 1) / parts;
-      for (int i = 0; i < parts; ++i) atomicAdd(&s_bin[bin_of(min(per, q.x1 - i * per))], 1);
-    }
+  each([&](const QueryBlock &q) {
+    const int parts = parts_of(q.x1), per = (q.x1 + parts - 1) / parts;
+    for (int i = 0; i < parts; ++i) atomicAdd(&s_bin[bin_of(min(per, q.x1 - i * per))], 1);
+  });
   __syncthreads();
   // exclusive scan of the bins, kBins / kExpandThreads to a thread
   constexpr int PER = kBins / kExpandThreads;
@@ -201,22 +208,21 @@ __device__ void list_query_blocks(const KvAttnArgs &a, const Expanded &x) {
     x.counters[1] = 0;
   }
   __syncthreads();
-  for (int slot = tid; slot < x.slots; slot += kExpandThreads)
-    if (block_of(slot, q)) {
-      const int count = q.x1, parts = parts_of(count), per = (count + parts - 1) / parts;
-      if (parts > 1) {
-        q.slot = atomicAdd(&s_count[1], parts);
-        q.parts = parts;
-        x.split[atomicAdd(&s_count[0], 1)] = q;
-      }
-      const int slot0 = q.slot;
-      for (int i = 0; i < parts; ++i) {
-        if (parts > 1) q.slot = slot0 + i;
-        q.x0 = i * per;
-        q.x1 = min(count, q.x0 + per);
-        x.blocks[atomicAdd(&s_bin[bin_of(q.x1 - q.x0)], 1)] = q;
-      }
+  each([&](QueryBlock q) {
+    const int count = q.x1, parts = parts_of(count), per = (count + parts - 1) / parts;
+    if (parts > 1) {
+      q.slot = atomicAdd(&s_count[1], parts);
+      q.parts = parts;
+      x.split[atomicAdd(&s_count[0], 1)] = q;
     }
+    const int slot0 = q.slot;
+    for (int i = 0; i < parts; ++i) {
+      if (parts > 1) q.slot = slot0 + i;
+      q.x0 = i * per;
+      q.x1 = min(count, q.x0 + per);
+      x.blocks[atomicAdd(&s_bin[bin_of(q.x1 - q.x0)], 1)] = q;
+    }
+  });
   __syncthreads();
   if (tid == 0) x.counters[2] = s_count[0];
 }
@@ -948,10 +954,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv_prefill_join_kernel(const __g
 
 int64_t query_block_slots(const KvAttnArgs &a) { return a.s.tokens / (2 * (kRows / a.group)) + a.s.batch; }
 
-// Whether blocks may be split: where there are not many more items than SMs.
-// (Measured: with 8 items an SM the longest-first order alone leaves the SMs
-// within 3 % of one another; with 2, an SM may wait for one item half the time.)
-bool may_split(const KvAttnArgs &a, int num_sms) { return query_block_slots(a) * a.c.heads <= 4 * num_sms; }
+// Whether blocks may be split: where there are not many more items than SMs,
+// and contexts longer than what a part has at least. Split : whole, us a call, 8
+// kv heads of 4: 256 tokens behind 16384 keys 134 : 253, with eight prompts of
+// 256 beside them 151 : 276, 512 behind 4096 73 : 81. Where nothing turns out
+// to be worth splitting, the sum over all blocks and the join's launch cost
+// 1 to 6: one prompt of 2048 51 : 48, eight of 512 in tables of 2048 54 : 48.
+bool may_split(const KvAttnArgs &a, int num_sms) {
+  return query_block_slots(a) * a.c.heads <= 4 * num_sms && expanded_len(a.s.max_kv) / kKeys > kMinShare + kMinOver;
+}
 
 int64_t part_bytes(const KvAttnArgs &a) { return int64_t(2) * kRows * (a.c.d + 2) * sizeof(float); }
 
