@@ -27,6 +27,15 @@
 // over the heads of a row at a time.
 //   The read-back takes a warp per (granule of 16 positions, head), whose
 // codes of k and of v are each one run of 16 D bytes.
+//
+// Measured (device time, back to back over buffers larger than L2 together):
+// the append of 8192 tokens of 8 heads of 128 with 32 query heads rotated
+// moves 190 MB in 38.8 us, 4.9 TB/s; at that point the SMs issue in 61 % of
+// cycles and DRAM is 46 % busy, so what is left is latency between a row's
+// loads and the work on them. Five prompts of up to 1531 tokens with pages of
+// 16: 28.6 us. A step of 32 tokens x 32 heads: 3.5 us, a launch and five dependent
+// loads. The read-back of 32768 tokens of 8 heads moves 201 MB in 35 us,
+// 5.7 TB/s, 0.87 of what a copy reaches.
 #include "kv_common.cuh"
 
 namespace w8a8 {

@@ -50,6 +50,16 @@
 // memory, so that there are few parts (kv_decode_block_kernel). Where they are
 // few and short a block has a segment, and there is nothing to join: one
 // launch. The rules and what they measured stand at the host's choice below.
+//
+// Measured (device time, back to back): 32 sequences x 32 heads x 4096 keys of
+// 128 (1.07 GB of codes) 189 to 193 us, 5.6 TB/s; 64 sequences of 1 to 32768
+// keys, 8 heads for 32 (547 MB) 103 us, 5.3 TB/s: the rate of a stream that is
+// only read (5.3 to 5.7 TB/s here, where a copy moves 6.6). Alone in a profile
+// the first takes 168 us: the SMs issue in 57 % of cycles, the ALU pipe in
+// 51 %, the tensor pipe is 20 % busy. Scores by s8 products (codes as they lie,
+// q as 22-bit fixed point in three int8 parts) need a sixth fewer
+// instructions and measured 192 to 202 and 103.5 us: not the limit. The
+// smallest calls are their latency: one sequence of 512 keys 8.0 us.
 #include "kv_common.cuh"
 
 namespace w8a8 {
