@@ -352,6 +352,73 @@ def test_bad_pages_and_sequences_are_reported_and_skipped():
     assert_cache(c, cache)
 
 
+@pytest.mark.parametrize("new,ctx", [([1, 1, 1], [40, 300, 7]), ([5, 12, 1], [0, 90, 33]), ([70, 33, 129], [100, 0, 15])])
+@pytest.mark.parametrize("d,page,hq,hkv", [(128, 32, 8, 2), (96, 16, 3, 3), (64, 64, 5, 1)])
+def test_attention_query_strides(new, ctx, d, page, hq, hkv):
+    """Queries inside a fused projection's rows, and head-major: the same bits as dense ones."""
+    rng = np.random.default_rng(d + new[0])
+    s, pages = R.make_seqs(rng, new, ctx, page, spare=1)
+    cache = R.random_cache(rng, pages, hkv, page, d)
+    q, args, out = check_attention(rng, s, cache, hq)
+    n = int(s.start[-1])
+    fused = torch.full((s.tokens, hq + 2 * hkv + 1, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    fused[:, 1:1 + hq] = dev_bf16(q)
+    heads_first = dev_bf16(q).transpose(0, 1).contiguous().transpose(0, 1)
+    for view in (fused[:, 1:1 + hq], heads_first):
+        got = W.w8a8_kv_attention(view, to_dev(cache), batch_of(s), **args)
+        assert torch.equal(got[:n], out[:n])
+    assert status() == 0
+
+
+@pytest.mark.parametrize("new", [(1, 3, 2), (40, 70, 9)])
+def test_rows_in_front_of_the_first_sequence_are_nobodys(new):
+    rng = np.random.default_rng(new[0])
+    s, pages = R.make_seqs(rng, list(new), [20, 0, 70], 16, spare=2)
+    s = R.Seqs(s.table, s.start + 21, s.kv, spare=2)
+    cache = R.random_cache(rng, pages, 2, 16, 64)
+    check_attention(rng, s, cache, 4)
+    x = bf16_rows(rng, s.tokens, 2, 64)
+    c = to_dev(cache)
+    keep = dev_bf16(bf16_rows(rng, s.tokens, 2, 64))
+    q_out = keep.clone()
+    W.w8a8_kv_append(dev_bf16(x), dev_bf16(x), c, batch_of(s), q=dev_bf16(x), q_out=q_out)
+    f = synth.bits_to_f32(x)
+    assert_cache(c, R.append(cache, s, f, f))
+    first, last = int(s.start[0]), int(s.start[-1])
+    assert torch.equal(q_out[:first], keep[:first]) and torch.equal(q_out[last:], keep[last:])
+    assert torch.equal(q_out[first:last], dev_bf16(x)[first:last])
+    assert status() == 0
+
+
+@pytest.mark.parametrize("hq,new", [(2, 1), (2, 40), (64, 3)])
+def test_a_call_whose_contexts_are_all_empty(hq, new):
+    c = W.PagedKVCache.empty(4, 2, 16, 64)
+    rows = 3 * new
+    b = W.KVBatch(torch.zeros((3, 2), dtype=torch.int32, device="cuda"), dev(np.arange(4, dtype=np.int32) * new),
+                  torch.zeros(3, dtype=torch.int32, device="cuda"), new, 0)
+    x = torch.ones((rows, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.ones((rows, hq, 64), dtype=torch.bfloat16, device="cuda")
+    turned = W.w8a8_kv_append(x, x, c, b, q=q)
+    assert not turned.any() and not c.k_codes.any() and not c.k_scale.any()
+    assert not W.w8a8_kv_attention(q, c, b).any()
+    assert status() == 0
+
+
+def test_many_sequences():
+    """More sequences than a warp scans at once, for each of the kernels."""
+    rng = np.random.default_rng(21)
+    for new, ctx in (([1, 0, 2] * 400, [3, 17, 40] * 400), ([70, 1, 0] * 40, [5, 40, 3] * 40)):
+        s, pages = R.make_seqs(rng, new, ctx, 16, spare=1)
+        cache = R.random_cache(rng, pages, 1, 16, 64)
+        check_attention(rng, s, cache, 2)
+        x = bf16_rows(rng, s.tokens, 1, 64)
+        c = to_dev(cache)
+        W.w8a8_kv_append(dev_bf16(x), dev_bf16(x), c, batch_of(s))
+        f = synth.bits_to_f32(x)
+        assert_cache(c, R.append(cache, s, f, f))
+    assert status() == 0
+
+
 @pytest.mark.parametrize("new", [(1, 1, 1), (70, 33, 129)])
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 100, 600])
 def test_a_window_of_all_positions_is_none(new, window):
