@@ -42,8 +42,9 @@
 // are cut into equal pieces, whatever the lengths of the sequences, which only
 // the device knows. A piece that holds all of a segment writes its output;
 // parts go to the workspace (sums, references, sum of weights) and
-// kv_join_kernel joins them in the order of the pieces. The same arithmetic on
-// the lengths tells it who has what.
+// kv_join_kernel joins them in the order of the pieces. Every warp finds its
+// piece by a scan over the sequences' lengths, and the join who has what: by
+// the same scan, or, of many sequences, from what one warp left of it.
 //   A piece is one warp's, so that warps start segments while others stream
 // (kv_decode_kernel). Where segments are few and long it is that of a block of
 // all an SM's warps, which deal its tiles out among them and join in shared
@@ -219,11 +220,13 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t v) {  // inclusive
 }
 
 // Units before sequence `b` (if it is one) and all units; called by a whole
-// warp. Returns the lane's inclusive scan of the last 32 sequences. (Fewer
-// than 2^31 units in all: the host has checked it.)
+// warp. Returns the lane's inclusive scan of the last 32 sequences. The one
+// warp that is given `offsets` leaves the units before each sequence there,
+// and all of them behind the last. (Fewer than 2^31 units in all: the host has
+// checked it.)
 template <int ROWS, int SETUP>
-__device__ __forceinline__ uint32_t count_units(const KvAttnArgs &a, int32_t b, int32_t *status, uint32_t &before,
-                                                uint32_t &all) {
+__device__ __forceinline__ uint32_t count_units(const KvAttnArgs &a, int32_t b, int32_t *status, uint32_t *offsets,
+                                                uint32_t &before, uint32_t &all) {
   const int lane = threadIdx.x & 31;
   uint32_t sum = 0;
   before = all = 0;
@@ -232,8 +235,10 @@ __device__ __forceinline__ uint32_t count_units(const KvAttnArgs &a, int32_t b, 
     const uint32_t v = i < a.s.batch ? seq_work<ROWS, SETUP>(a, i, status).units() : 0;
     sum = warp_scan(v);
     if (b >= i0 && b < i0 + 32) before = all + __shfl_sync(0xFFFFFFFFu, sum - v, b - i0);
+    if (offsets && i < a.s.batch) offsets[i] = all + sum - v;
     all += __shfl_sync(0xFFFFFFFFu, sum, 31);
   }
+  if (offsets && lane == 0) offsets[a.s.batch] = all;
   return sum;
 }
 
@@ -672,7 +677,7 @@ struct Joined {
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, sm_warps(NT) / kWarps)
-    kv_decode_kernel(const __grid_constant__ KvAttnArgs a, float *__restrict__ partial) {
+    kv_decode_kernel(const __grid_constant__ KvAttnArgs a, float *__restrict__ partial, uint32_t *__restrict__ offsets) {
   constexpr int MT = D / 16, ROWS = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -680,7 +685,8 @@ __global__ void __launch_bounds__(kThreads, sm_warps(NT) / kWarps)
   pdl_launch_dependents();  // after the wait: the join may read the lengths before its own
   uint32_t all, before;
   const uint32_t p = warp * gridDim.x + blockIdx.x;  // few pieces spread over all SMs
-  const uint32_t sum = count_units<ROWS, kSetup>(a, -1, p == 0 ? a.status : nullptr, before, all);
+  const uint32_t sum =
+      count_units<ROWS, kSetup>(a, -1, p == 0 ? a.status : nullptr, p == 0 ? offsets : nullptr, before, all);
   if (all == 0) return;
   const Cut cut(all, gridDim.x * kWarps, kMinUnits);
   if (p >= cut.pieces) return;
@@ -717,8 +723,8 @@ __global__ void __launch_bounds__(kThreads, sm_warps(NT) / kWarps)
 // block, sequence) has that segment; else the units are cut over the blocks.
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * sm_warps(NT), 1)
-    kv_decode_block_kernel(const __grid_constant__ KvAttnArgs a, float *__restrict__ partial, int per_segment,
-                           int row_blocks) {
+    kv_decode_block_kernel(const __grid_constant__ KvAttnArgs a, float *__restrict__ partial,
+                           uint32_t *__restrict__ offsets, int per_segment, int row_blocks) {
   using C = Cfg<D>;
   constexpr int ROWS = 8 * NT, F = partial_floats<D, NT>(), BW = sm_warps(NT);
   static_assert(F * sizeof(float) <= kStages * C::kStage, "a warp's sums fit its ring");
@@ -769,7 +775,9 @@ __global__ void __launch_bounds__(32 * sm_warps(NT), 1)
   }
   uint32_t all, before;
   const uint32_t p = blockIdx.x;
-  const uint32_t sum = count_units<ROWS, kBlockSetup>(a, -1, p == 0 && warp == 0 ? a.status : nullptr, before, all);
+  const bool first = p == 0 && warp == 0;
+  const uint32_t sum =
+      count_units<ROWS, kBlockSetup>(a, -1, first ? a.status : nullptr, first ? offsets : nullptr, before, all);
   if (all == 0) return;
   const Cut cut(all, gridDim.x, kBlockMinUnits);
   if (p >= cut.pieces) return;
@@ -785,7 +793,7 @@ __global__ void __launch_bounds__(32 * sm_warps(NT), 1)
 // segment that one piece holds is written already; one without keys is zeros.
 template <int D, int NT, int SETUP>
 __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_constant__ KvAttnArgs a,
-                                                                  const float *__restrict__ partial,
+                                                                  const float *partial, const uint32_t *offsets,
                                                                   uint32_t most_pieces, uint32_t min_units,
                                                                   int max_rows) {
   constexpr int ROWS = 8 * NT, F = partial_floats<D, NT>();
@@ -794,9 +802,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y;
   const int h = blockIdx.x / max_rows, row = blockIdx.x % max_rows;
-  // the lengths: written before the kernel that this one follows passed its own wait
   uint32_t before, all;
-  count_units<ROWS, SETUP>(a, b, nullptr, before, all);
+  if (offsets) {
+    pdl_wait_prerequisite();
+    before = offsets[b], all = offsets[a.s.batch];
+  } else {  // the lengths: written before the kernel that this one follows passed its own wait
+    count_units<ROWS, SETUP>(a, b, nullptr, nullptr, before, all);
+  }
   const SeqWork<SETUP> work = seq_work<ROWS, SETUP>(a, b, nullptr);
   const Cut cut(all, most_pieces, min_units);
   const int rbs = work.segs / a.c.heads;
@@ -807,7 +819,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
     p1 = cut.piece_of(s0 + work.seg_units() - 1);
   }
   pdl_launch_dependents();
-  pdl_wait_prerequisite();
+  if (!offsets) pdl_wait_prerequisite();
   if (row >= work.seq.q * a.group || (work.walk.count > 0 && p0 == p1)) return;
   Joined y;
   if (work.walk.count > 0) {
@@ -880,9 +892,25 @@ bool block_pieces(const KvAttnArgs &a, int num_sms) {
   return !wide_rows(a) && segs <= 2 * num_sms && segs * (a.s.max_kv / kTile) >= kBlockTiles * num_sms;
 }
 
+// Sequences up to which each block of the join finds the units before its own
+// by a scan, while the kernel before it ends; with more it reads what that
+// kernel's first warp has left in the workspace, once it has ended. Scan : read,
+// us a call, 4 kv heads of 4, 200 and 1500 keys: 64 sequences 15.7 28.1 : 16.2
+// 27.0, 96 18.1 38.6 : 17.7 38.4, 128 22.9 48.0 : 20.8 46.6, 256 40 91 : 30 82,
+// 1024 283 462 : 99 282 (the scan's cost grows with the square).
+constexpr int32_t kScanSequences = 96;
+
+// The parts in the workspace, two a piece; the units before each sequence follow them.
+int64_t partials_floats(const KvAttnArgs &a, int num_sms) {
+  const int64_t pieces = block_pieces(a, num_sms) ? num_sms : static_cast<int64_t>(num_sms) * sm_warps(wide_rows(a) ? 2 : 1);
+  return 2 * pieces * (wide_rows(a) ? 16 : 8) * (a.c.d + 4);
+}
+
 template <int D, int NT>
 cudaError_t launch_t(const KvAttnArgs &a, float *partial, int num_sms, cudaStream_t s) {
   using C = Cfg<D>;
+  uint32_t *const offsets =
+      a.s.batch > kScanSequences ? reinterpret_cast<uint32_t *>(partial + partials_floats(a, num_sms)) : nullptr;
   constexpr size_t kBlockSmem = C::kSmem / kWarps * sm_warps(NT);
   static_assert(kBlockSmem <= 227 * 1024, "shared memory per CTA");
   cudaLaunchConfig_t cfg = {};
@@ -901,13 +929,13 @@ cudaError_t launch_t(const KvAttnArgs &a, float *partial, int num_sms, cudaStrea
     cfg.gridDim = per_segment ? dim3(a.c.heads * row_blocks, a.s.batch) : dim3(num_sms);
     cfg.blockDim = dim3(32 * sm_warps(NT));
     cfg.dynamicSmemBytes = kBlockSmem;
-    e = cudaLaunchKernelEx(&cfg, kv_decode_block_kernel<D, NT>, a, partial, per_segment ? 1 : 0, row_blocks);
+    e = cudaLaunchKernelEx(&cfg, kv_decode_block_kernel<D, NT>, a, partial, offsets, per_segment ? 1 : 0, row_blocks);
     if (e != cudaSuccess || per_segment) return e;
     cfg.gridDim = join_grid;
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, kBlockSetup>, a, static_cast<const float *>(partial),
-                              static_cast<uint32_t>(num_sms), static_cast<uint32_t>(kBlockMinUnits), max_rows);
+                              static_cast<const uint32_t *>(offsets), static_cast<uint32_t>(num_sms), static_cast<uint32_t>(kBlockMinUnits), max_rows);
   }
   cudaError_t e = ensure_kernel_smem<kv_decode_kernel<D, NT>>(static_cast<int>(C::kSmem), true);
   if (e != cudaSuccess) return e;
@@ -915,13 +943,13 @@ cudaError_t launch_t(const KvAttnArgs &a, float *partial, int num_sms, cudaStrea
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   const uint32_t warps = cfg.gridDim.x * kWarps;
-  e = cudaLaunchKernelEx(&cfg, kv_decode_kernel<D, NT>, a, partial);
+  e = cudaLaunchKernelEx(&cfg, kv_decode_kernel<D, NT>, a, partial, offsets);
   if (e != cudaSuccess) return e;
   cfg.gridDim = join_grid;
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, kSetup>, a, static_cast<const float *>(partial), warps,
-                            static_cast<uint32_t>(kMinUnits), max_rows);
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, NT, kSetup>, a, static_cast<const float *>(partial),
+                            static_cast<const uint32_t *>(offsets), warps, static_cast<uint32_t>(kMinUnits), max_rows);
 }
 
 template <int D>
@@ -937,13 +965,13 @@ bool kv_decode_fits(const KvAttnArgs &a) {  // all units in 31 bits
 }
 
 size_t kv_decode_workspace_bytes(const KvAttnArgs &a, int num_sms) {
-  // Two parts a piece; none where a block has a segment. (The query knows no
-  // window and no prefix: what it says is enough for any.)
+  // None where a block has a segment. (The query knows no window and no
+  // prefix: what it says is enough for any.)
   KvAttnArgs any = a;
   any.window = 0;
   if (block_segments(any, num_sms)) return 0;
-  const int64_t pieces = block_pieces(a, num_sms) ? num_sms : static_cast<int64_t>(num_sms) * sm_warps(wide_rows(a) ? 2 : 1);
-  return static_cast<size_t>(2 * pieces * (wide_rows(a) ? 16 : 8) * (a.c.d + 4)) * sizeof(float);
+  return static_cast<size_t>(partials_floats(a, num_sms)) * sizeof(float) +
+         (a.s.batch > kScanSequences ? (a.s.batch + 1) * sizeof(uint32_t) : 0);
 }
 
 cudaError_t launch_kv_decode(const KvAttnArgs &a, void *workspace, int num_sms, cudaStream_t s) {

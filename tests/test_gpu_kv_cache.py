@@ -251,6 +251,15 @@ def test_attention_few_long_blocks(d, page, hq, hkv, mask):
     check_attention(rng, s, R.random_cache(rng, pages, hkv, page, d), hq, **mask_args(mask, hq))
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 95, 96, 97, 129])
+def test_attention_single_tokens_of_several_scans_of_sequences(B):
+    rng = np.random.default_rng(B)
+    ctx = [int(c) for c in rng.integers(0, 90, B)]
+    ctx[B // 2] = 2100  # cut into parts
+    s, pages = R.make_seqs(rng, [1] * B, ctx, 32, kv=[0 if b % 7 == 3 else ctx[b] + 1 for b in range(B)], spare=1)
+    check_attention(rng, s, R.random_cache(rng, pages, 2, 32, 64), 4, prefix=rng.integers(0, 99, B).astype(np.int32))
+
+
 @pytest.mark.parametrize("mask", ["plain", "softcap", "window_33", "window_prefix", "all"])
 @pytest.mark.parametrize("new,ctx,hq,hkv", [
     ([33, 1, 64], [100, 700, 0], 1, 1), ([11, 16, 2], [40, 0, 1200], 8, 2), ([1, 3, 2], [5, 900, 63], 21, 1),
