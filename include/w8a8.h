@@ -561,7 +561,10 @@ typedef struct w8a8_kv_scores {
  *   workspace  device, >= w8a8_kv_attention_workspace_size(...) bytes,
  *          16-byte aligned; no initial contents needed, and calls that may
  *          overlap on the GPU must not share it
- * q_heads is a multiple of kv_heads, at most 128 times it. The result does
+ * q_heads is a multiple of kv_heads, at most 128 times it. Batches whose
+ * bounds allow more than 2^31 units of work (key tiles of all kv heads and
+ * sequences at max_kv_len, for each 8 or 16 query rows; or that many expanded
+ * keys) are refused with W8A8_ERR_UNSUPPORTED_SHAPE. The result does
  * not depend on what else runs on the device: partial results are joined in
  * a fixed order.
  */
