@@ -533,14 +533,27 @@ class PagedKVCache:
         return cls(*codes, *scales)
 
 
+def _page_table(t) -> int:
+    """The row stride of an int32 [batch, max_pages] page table. (Of one row or none torch may report any stride;
+    the C calls want at least the row's length. Rows that overlap are no table the kernels can walk.)"""
+    ld = _rows(t, torch.int32, "page_table")
+    if ld >= t.shape[1]:
+        return ld
+    if t.shape[0] > 1:
+        raise ValueError(f"page_table: rows overlap (shape {tuple(t.shape)} strides {tuple(t.stride())}); "
+                         "sequences that share pages need a row each, as .contiguous() makes them")
+    return t.shape[1]
+
+
 class KVBatch:
     """The sequences of a call (w8a8_kv_batch): page_table int32 [batch,
-    max_pages] (rows contiguous), seq_start int32 [batch + 1], kv_len int32
-    [batch], all on the device and read there, and the host's bounds on a
-    sequence's new tokens and length. Checked once here."""
+    max_pages] (rows contiguous, at any distance that keeps them apart),
+    seq_start int32 [batch + 1], kv_len int32 [batch], all on the device and
+    read there, and the host's bounds on a sequence's new tokens and length.
+    Checked once here."""
 
     def __init__(self, page_table, seq_start, kv_len, max_q_len: int, max_kv_len: int | None = None):
-        ld = _rows(page_table, torch.int32, "page_table")
+        ld = _page_table(page_table)
         batch, max_pages = page_table.shape
         _vec(seq_start, torch.int32, batch + 1, "seq_start")
         _vec(kv_len, torch.int32, batch, "kv_len")
@@ -549,8 +562,8 @@ class KVBatch:
         if seq_start.device != page_table.device or kv_len.device != page_table.device:
             raise ValueError("expected page_table, seq_start and kv_len on one device")
         self.size, self._max_pages = batch, max_pages
-        self._fields = (page_table.data_ptr(), max(ld, max_pages), seq_start.data_ptr(), kv_len.data_ptr(), batch,
-                        max_pages, self.max_q_len)
+        self._fields = (page_table.data_ptr(), ld, seq_start.data_ptr(), kv_len.data_ptr(), batch, max_pages,
+                        self.max_q_len)
         self._refs = {}
 
     def _for(self, cache: PagedKVCache):
@@ -680,7 +693,7 @@ def w8a8_kv_gather(cache: PagedKVCache, page_table, first_pos, row_start, rows: 
     row_start[b] .. row_start[b + 1] of k_out and v_out [rows, kv_heads,
     head_dim] (bf16 or fp32; both allocated for `rows` rows when neither is
     given) -> (k_out, v_out)."""
-    ld = _rows(page_table, torch.int32, "page_table")
+    ld = _page_table(page_table)
     batch, max_pages = page_table.shape
     _dense(first_pos, torch.int32, (batch,), "first_pos")
     _dense(row_start, torch.int32, (batch + 1,), "row_start")
@@ -701,8 +714,8 @@ def w8a8_kv_gather(cache: PagedKVCache, page_table, first_pos, row_start, rows: 
         if k_out is not None and v_out is not None:
             _dense(v_out, given.dtype, shape, "v_out")
     _same_gpu(cache._dev, page_table, first_pos, row_start, k_out, v_out)
-    _kv_call("w8a8_kv_gather", cache._dev, stream, cache._ref, page_table.data_ptr(), ld if ld > max_pages else max_pages,
-             batch, max_pages, first_pos.data_ptr(), row_start.data_ptr(), shape[0],
+    _kv_call("w8a8_kv_gather", cache._dev, stream, cache._ref, page_table.data_ptr(), ld, batch, max_pages,
+             first_pos.data_ptr(), row_start.data_ptr(), shape[0],
              None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
              BF16 if given.dtype is torch.bfloat16 else FP32)
     return k_out, v_out

@@ -1,0 +1,42 @@
+"""What the binding of the INT8 paged KV cache hands to the C calls, on a host
+without a GPU: row strides of page tables."""
+import pytest
+import torch
+
+from int8_gemm_token_b200 import w8a8 as W
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+# ------------------------------------------------------------------ page tables whose rows lie in one another
+OVERLAPPING = {
+    "one row for all": lambda: i32(1, 4).expand(3, 4),
+    "one entry for all": lambda: i32(1, 1).expand(3, 1),
+    "rows one apart": lambda: i32(6).as_strided((3, 4), (1, 1)),
+    "rows three apart": lambda: i32(10).as_strided((3, 4), (3, 1)),
+}
+
+
+@pytest.mark.parametrize("table", OVERLAPPING)
+def test_tables_whose_rows_overlap_are_refused(table):
+    """Their rows are not max_pages apart: read so, they end past the tensor."""
+    t = OVERLAPPING[table]()
+    cache = W.PagedKVCache.empty(4, 2, 16, 64, "cpu")
+    with pytest.raises(ValueError, match="page_table.*overlap"):
+        W.KVBatch(t, i32(4), i32(3), 1)
+    with pytest.raises(ValueError, match="page_table.*overlap"):
+        W.w8a8_kv_gather(cache, t, i32(3), i32(4), rows=5)
+    W.KVBatch(t.contiguous(), i32(4), i32(3), 1)
+
+
+@pytest.mark.parametrize("table,ld", [
+    (lambda: i32(3, 4), 4), (lambda: i32(3, 9)[:, 2:6], 9), (lambda: i32(6, 4)[::2], 8), (lambda: i32(1, 4).expand(1, 4), 4),
+    (lambda: i32(8).as_strided((1, 4), (1, 1)), 4), (lambda: i32(3, 0), 1), (lambda: i32(0, 4), 4)])
+def test_the_row_stride_of_a_table_is_its_own(table, ld):
+    """Of one row (or none) any stride is as good as the row's length."""
+    t = table()
+    b = W.KVBatch(t, i32(t.shape[0] + 1), i32(t.shape[0]), 1)
+    c = b._for(W.PagedKVCache.empty(4, 2, 16, 64, "cpu"))._obj
+    assert c.page_table_ld == ld >= t.shape[1]
