@@ -447,8 +447,11 @@ size_t int8_mixed_decomp_gemm_tc_workspace_size(int64_t M, int64_t N, int32_t ca
  * the device status word (so does a seq_start that descends, after which it
  * is left open which sequences are served); a page table entry outside
  * [0, num_pages) that is needed sets W8A8_ERR_BAD_PAGE, is not dereferenced,
- * and its tokens are neither stored nor seen (read back as 0). Entries past
- * a sequence's last page are not read.
+ * and its tokens are neither stored nor seen (read back as 0). An append needs
+ * the pages that receive tokens, a read-back those of its range, an attention
+ * those of which some new token of the sequence sees a position: entries of
+ * pages that a window has left behind, like those past a sequence's last page,
+ * are not read.
  *
  * Several sequences may share pages that a call only reads. A page that
  * w8a8_kv_append writes must belong to one sequence.

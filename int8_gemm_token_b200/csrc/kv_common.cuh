@@ -97,6 +97,14 @@ __device__ __forceinline__ TileWalk tile_walk(int tile, int prefix, int n, int f
   return w;
 }
 
+// Whether some query of a sequence of n keys, whose first query is at position
+// `first`, sees a key of the granule that begins at `key` (a tile of a walk
+// may begin in front of the window's edge or end behind the prefix). The page
+// of any other granule is not looked at: its entry may say anything.
+__device__ __forceinline__ bool granule_seen(int key, int prefix, int n, int first, int window) {
+  return key < n && (key < prefix || window == 0 || key + kGran > first - window + 1);
+}
+
 // Final values of neighbouring output elements.
 __device__ __forceinline__ void store_out2(const KvAttnArgs &a, int64_t elem, float y0, float y1) {
   const uint32_t b = pack_bf16x2(y0, y1);

@@ -403,10 +403,10 @@ __device__ __forceinline__ void attend(const KvAttnArgs &a, const KvSeq &seq, co
   float ks_c, vs_c, ks_n, vs_n;
   const auto fetch = [&](int x) {  // tiles x .. x + 15
     page_n = -1;
-    ks_n = -1.0f;  // (no page)
+    ks_n = -1.0f;  // (no page, or none that is seen)
     vs_n = -INFINITY;
     const int key = walk.tile(x + (lane >> 1)) * kTile + (lane & 1) * kGran;
-    if (x + (lane >> 1) >= x1 || key >= seq.n) return;
+    if (x + (lane >> 1) >= x1 || !granule_seen(key, prefix, seq.n, max(seq.pos0(), 0), a.window)) return;
     page_n = load_page(table_row, key >> a.c.page_shift, a.c.pages, a.status);
     if (page_n < 0) return;
     const int64_t i = static_cast<int64_t>(page_n) * a.c.heads + h;

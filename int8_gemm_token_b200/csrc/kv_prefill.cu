@@ -92,8 +92,9 @@ int64_t expanded_len(int32_t max_kv) { return (static_cast<int64_t>(max_kv) + kK
 // ------------------------------------------------------------------ expansion
 // Block (x > 0): 64 keys of one (kv head, sequence). Rows from the sequence's end to
 // the end of its last 128-key tile are zeros (they meet weights of 0, and
-// must not be NaN). A granule's scales: of its page; 0 past the end; -1 for a
-// page that does not exist.
+// must not be NaN). A granule's scales: of its page; 0 past the end; -1 (k's)
+// for a page that does not exist or of which no query sees a key there, and
+// whose codes are then zeros.
 constexpr int kExpandKeys = 64;
 constexpr int kExpandThreads = 256;
 
@@ -264,7 +265,8 @@ __global__ void __launch_bounds__(kExpandThreads, 6) kv_expand_kernel(const __gr
     int32_t page = -1;
     float ks = 0.0f, vs = 0.0f;
     if (key < seq.n) {
-      page = load_page(a.s.table + b * a.s.table_ld, key >> a.c.page_shift, a.c.pages, a.status);
+      if (granule_seen(key, prefix, seq.n, max(seq.pos0(), 0), a.window))
+        page = load_page(a.s.table + b * a.s.table_ld, key >> a.c.page_shift, a.c.pages, a.status);
       ks = page < 0 ? -1.0f : __ldg(a.c.ks + static_cast<int64_t>(page) * a.c.heads + h);
       vs = page < 0 ? 0.0f : __ldg(a.c.vs + static_cast<int64_t>(page) * a.c.heads + h);
     }
