@@ -430,7 +430,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   if (!gather_ok(a, r0, r1, first)) return;
   const int64_t granule = first / kGran + (slot - f(b));
   const int end = first + (r1 - r0);  // one past the last position
-  if (slot < f(b) || granule * kGran >= end) return;  // (as in append_pages_kernel)
+  // (the first as in append_pages_kernel; an empty range may begin inside a granule)
+  if (slot < f(b) || r1 == r0 || granule * kGran >= end) return;
   const int key0 = static_cast<int>(granule) * kGran;
   const int32_t page = load_page(a.table + b * a.table_ld, key0 >> a.c.page_shift, a.c.pages, a.status);
   const int64_t block = static_cast<int64_t>(max(page, 0)) * a.c.heads + h;

@@ -1,5 +1,5 @@
 """The INT8 paged KV cache on the GPU at its edges: table entries that no call
-needs."""
+needs, ranges of nothing."""
 import numpy as np
 import pytest
 import torch
@@ -60,3 +60,20 @@ def test_entries_of_pages_that_a_query_sees_are_needed(new, at):
     W.w8a8_kv_attention(dev_bf16(bf16_rows(rng, s.tokens, 4, 64)), cache, batch_of(s), window=144 - new - 63 + 1,
                         prefix_len=dev(np.array([17], np.int32)))
     assert status() == 11
+
+
+# ------------------------------------------------------------------ nothing to read
+@pytest.mark.parametrize("first", [5, 15, 16, 17, 40])
+def test_an_empty_range_reads_no_page(first):
+    rng = np.random.default_rng(first)
+    cache = to_dev(R.random_cache(rng, 4, 2, 16, 64))
+    table = np.full((3, 4), -1, np.int32)
+    table[2, :2] = 3, 1
+    ko = torch.full((9, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert status() == 0
+    W.w8a8_kv_gather(cache, dev(table), dev(np.array([first, first, 13], np.int32)), dev(np.array([0, 0, 0, 9], np.int32)),
+                     k_out=ko)
+    assert status() == 0
+    x = cache.k_codes.float() * cache.k_scale[:, :, None, None]
+    want = torch.cat([x[3, :, 13:], x[1, :, :6]], 1).transpose(0, 1).bfloat16()
+    assert torch.equal(ko, want)
