@@ -556,7 +556,7 @@ typedef struct w8a8_kv_scores {
  * once for the second product, by the query rows of a kv head (max_q_len *
  * (q_heads / kv_heads)): for up to 32, and up to 64 where batch * kv_heads <= 64
  * or max_kv_len >= 4096, to fp16 against the row's largest (2^-11 of the value,
- * at least 2^-25 of the largest); for more to bf16 (2^-8 of the value). A
+ * at least 2^-32 of the largest); for more to bf16 (2^-8 of the value). A
  * capped score is off by about softcap * 2^-22.
  *   q      device bf16 [tokens, q_heads, head_dim], strides in elements
  *          (multiples of 8, and not 0 where the axis has several elements)

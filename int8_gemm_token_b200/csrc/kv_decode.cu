@@ -21,12 +21,15 @@
 // element is in [2^14, 2^15) (elements 2^-29 below it start to lose bits), and
 // the weights 2^s_j times v's scale against a running reference of their own,
 // apart from that of the scores:
-//   w_j = 2^(s_j + log2 vs_j - mv),  l = sum_j 2^(s_j - m) in fp32,
-//   out = 2^(mv - m) (sum_j w_j code_j) / l.
+//   w_j = 2^(s_j + log2 vs_j - mv + 7),  l = sum_j 2^(s_j - m) in fp32,
+//   out = 2^(mv - m - 7) (sum_j w_j code_j) / l.
 // w_j is rounded to fp16 once (2^-11). m and mv follow the maxima of s_j and of
 // s_j + log2 vs_j only when these have outgrown them by 2^8, which a vote over
 // the warp's elements finds; only then are maxima exchanged between lanes and
-// the sums rescaled (weights stay below 2^8 and so below fp16's largest).
+// the sums rescaled. So w_j stays below 2^15, fp16's largest power of two, and
+// what fp16 cannot hold is below 2^-32 of the row's largest: l has every
+// weight, and a long tail that the sums lacked would be missing from the output
+// (2^18 keys of 2^-26 behind one of 1, in one piece: 0.4 % of it).
 //   Both contractions may run over their axis in any order as long as both
 // sides use the same one, so a lane reads its codes of K as 16 contiguous
 // bytes of one key and those of V as the same dims of four keys (pairs of
@@ -71,6 +74,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;     // keys of a tile: two granules, each of one page
 constexpr float kRescale = 8.0f;  // log2 of how far a maximum may outgrow its reference
+constexpr float kLift = 7.0f;     // log2 of the largest fp16 power of two, less kRescale
 // What a segment's start costs, in tiles, and units that a piece has at least:
 // of a piece of one warp, and of all of an SM's warps.
 constexpr int kSetup = 2, kMinUnits = 4;
@@ -354,9 +358,9 @@ __device__ __forceinline__ void store_part(float *part, int r, const RowState<D,
     *reinterpret_cast<float2 *>(part + r * D + v_dim<D>(g, i)) = make_float2(st.acc[i][nt][e], st.acc[i][nt][e + 2]);
 }
 
-// out = 2^(mv - m) sums / l; 0 where no key was seen
+// out = 2^(mv - m - kLift) sums / l; 0 where no key was seen
 __device__ __forceinline__ float final_factor(float m, float l, float mv) {
-  return l > 0.0f && mv != -INFINITY ? ex2(mv - m) / l : 0.0f;
+  return l > 0.0f && mv != -INFINITY ? ex2(mv - m) * exp2f(-kLift) / l : 0.0f;
 }
 
 // Key tiles number x0 .. x1 - 1 (at least one) of the walk of sequence b, for
@@ -483,7 +487,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs &a, const KvSeq &seq, co
       for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.0f;
   }
 
-  float fv[NT][2], fv_log = NAN;  // 2^(m + log2 vs - mv) for log2 vs = fv_log
+  float fv[NT][2], fv_log = NAN;  // 2^(m + log2 vs - mv + kLift) for log2 vs = fv_log
   const auto compute_tile = [&](int x, int slot, const float (&k_scale)[2], const float (&v_log)[2]) {
     const uint8_t *ks = ring + slot * C::kStage, *vs = ks + kTile * C::kPitch;
     const int key0 = walk.tile(x) * kTile;
@@ -589,8 +593,8 @@ __device__ __forceinline__ void attend(const KvAttnArgs &a, const KvSeq &seq, co
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            // (its exponent held in range: it is large only where 2^(s - m) is 0)
-            const float f = m[nt][e] + fv_log - mv[nt][e];
+            // (its exponent held in range: it passes 126 only where a page's scale is 2^100 times another's)
+            const float f = m[nt][e] + fv_log - mv[nt][e] + kLift;
             fv[nt][e] = mv[nt][e] == -INFINITY ? 0.0f : ex2(f > 126.0f ? 126.0f : f);
           }
       }

@@ -1,12 +1,13 @@
 """The INT8 paged KV cache on the GPU at its edges: table entries that no call
-needs, ranges of nothing."""
+needs, ranges of nothing, weights far below a row's largest."""
 import numpy as np
 import pytest
 import torch
 
+from int8_gemm_token_b200 import synth
 from int8_gemm_token_b200 import w8a8 as W
 from tests import kv_reference as R
-from tests.gpu_util import dev, dev_bf16
+from tests.gpu_util import dev, dev_bf16, host_bf16
 from tests.test_gpu_kv_cache import batch_of, bf16_rows, status, to_dev
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +78,38 @@ def test_an_empty_range_reads_no_page(first):
     x = cache.k_codes.float() * cache.k_scale[:, :, None, None]
     want = torch.cat([x[3, :, 13:], x[1, :, :6]], 1).transpose(0, 1).bfloat16()
     assert torch.equal(ko, want)
+
+
+# ------------------------------------------------------------------ weights far below the largest
+@pytest.mark.parametrize("B,hq,n", [(1776, 1, 1 << 18), (1, 1, 1 << 20), (1, 16, 1 << 20), (1, 1, 1000), (3, 1, 3000)])
+@pytest.mark.parametrize("log2_weight", [-26.0, -28.0])
+def test_small_weights_of_many_keys_add_up(B, hq, n, log2_weight):
+    """B sequences on the same pages, each: one key that takes nearly all the
+    weight and holds zeros, in front of a tail of equal keys that hold ones. T =
+    (n - 1) 2^log2_weight against the first key's 1 is the tail's, so the output
+    is T / (1 + T). Each weight keeps fp16's rounding of 2^-32 of the row's
+    largest, so the output is off by at most n 2^-32, and by its rounding to
+    bf16. The score is off by a few roundings of its 28 (2^-18), the exponential
+    by 2^-22. In the fp32 sum of the weights the one lane of eight that holds
+    the 1 may lose its keys of the tail (T / 8); the other lanes' roundings are
+    of sums of at most T (2^-13 with all the above)."""
+    page, d = 128, 64
+    pages = -(-n // page)
+    codes = [torch.zeros((pages, 1, page, d), dtype=torch.int8, device="cuda") for _ in range(2)]
+    k, v = codes
+    k[0, 0, 0, 0] = 64
+    v[:] = 1
+    v[0, 0, 0] = 0
+    ones = torch.ones((pages, 1), device="cuda")
+    q = torch.zeros((B, hq, d), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(B, pages).contiguous()
+    b = W.KVBatch(table, dev(np.arange(B + 1, dtype=np.int32)), dev(np.full(B, n, np.int32)), 1)
+    scale = -log2_weight * np.log(2.0) / 64
+    out = W.w8a8_kv_attention(q, W.PagedKVCache(k, v, ones, ones.clone()), b, scale=scale)
+    T = (n - 1) * np.exp(-64 * np.float64(np.float32(scale)))
+    want = T / (1 + T)
+    got = synth.bits_to_f32(host_bf16(out)).astype(np.float64)
+    tol = n * 2.0 ** -32 + want * (2.0 ** -8 + T / 8 + 2.0 ** -13)
+    assert (np.abs(got - want) <= tol).all(), (got.min(), got.max(), want, tol)
+    assert status() == 0
