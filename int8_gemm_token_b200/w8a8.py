@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 import re
 import threading
@@ -533,6 +534,12 @@ class PagedKVCache:
         return cls(*codes, *scales)
 
 
+def _bound(x) -> int:
+    """A host bound as the C int, which ctypes would cut to its low 32 bits: past the int's range the range's end
+    says the same (no sequence is that long)."""
+    return min(max(operator.index(x), -2 ** 31), 2 ** 31 - 1)
+
+
 def _page_table(t) -> int:
     """The row stride of an int32 [batch, max_pages] page table. (Of one row or none torch may report any stride;
     the C calls want at least the row's length. Rows that overlap are no table the kernels can walk.)"""
@@ -558,7 +565,7 @@ class KVBatch:
         _vec(seq_start, torch.int32, batch + 1, "seq_start")
         _vec(kv_len, torch.int32, batch, "kv_len")
         self.page_table, self.seq_start, self.kv_len = page_table, seq_start, kv_len
-        self.max_q_len, self.max_kv_len = int(max_q_len), max_kv_len
+        self.max_q_len, self.max_kv_len = _bound(int(max_q_len)), max_kv_len
         if seq_start.device != page_table.device or kv_len.device != page_table.device:
             raise ValueError("expected page_table, seq_start and kv_len on one device")
         self.size, self._max_pages = batch, max_pages
@@ -573,7 +580,7 @@ class KVBatch:
         ref = self._refs.get(cache.page_size)
         if ref is None:
             most = self._max_pages * cache.page_size if self.max_kv_len is None else int(self.max_kv_len)
-            ref = self._refs[cache.page_size] = ctypes.byref(_BatchStruct(*self._fields, most))
+            ref = self._refs[cache.page_size] = ctypes.byref(_BatchStruct(*self._fields, _bound(most)))
         return ref
 
 
@@ -726,8 +733,8 @@ def w8a8_kv_attention_workspace_size(cache: PagedKVCache, batch: KVBatch, tokens
     f = _kv_fn("w8a8_kv_attention_workspace_size")
     if cache._dev >= 0 and cache._dev != torch.cuda.current_device():
         with torch.cuda.device(cache._dev):
-            return f(cache._ref, batch._for(cache), tokens, q_heads)
-    return f(cache._ref, batch._for(cache), tokens, q_heads)
+            return f(cache._ref, batch._for(cache), tokens, _bound(q_heads))
+    return f(cache._ref, batch._for(cache), tokens, _bound(q_heads))
 
 
 def _attention(fn, q, cache, batch, scale, softcap, window, slopes, prefix_len, out, out_dtype, extra, workspace, stream):
@@ -753,7 +760,7 @@ def _attention(fn, q, cache, batch, scale, softcap, window, slopes, prefix_len, 
                 workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
     else:
         workspace, nbytes = _workspace(0, q.device, workspace)
-    sc = _ScoresStruct(d ** -0.5 if scale is None else scale, softcap, sp, window, pp)
+    sc = _ScoresStruct(d ** -0.5 if scale is None else scale, softcap, sp, _bound(window), pp)
     _kv_call(fn, dev, stream, cache._ref, batch._for(cache), tokens, q.data_ptr(), qst, qsh, hq, ctypes.byref(sc),
              *[t.data_ptr() for t in extra], out.data_ptr(), None if workspace is None else workspace.data_ptr(), nbytes)
     return out

@@ -1,5 +1,5 @@
 """What the binding of the INT8 paged KV cache hands to the C calls, on a host
-without a GPU: row strides of page tables."""
+without a GPU: row strides of page tables, bounds of any size."""
 import pytest
 import torch
 
@@ -40,3 +40,30 @@ def test_the_row_stride_of_a_table_is_its_own(table, ld):
     b = W.KVBatch(t, i32(t.shape[0] + 1), i32(t.shape[0]), 1)
     c = b._for(W.PagedKVCache.empty(4, 2, 16, 64, "cpu"))._obj
     assert c.page_table_ld == ld >= t.shape[1]
+
+
+# ------------------------------------------------------------------ host bounds past the C int
+@pytest.mark.parametrize("bound", [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63])
+def test_bounds_past_int32_stay_bounds(bound):
+    """As the C int they would be a small number, or a negative one."""
+    cache = W.PagedKVCache.empty(4, 2, 16, 64, "cpu")
+    c = W.KVBatch(i32(3, 4), i32(4), i32(3), bound)._for(cache)._obj
+    assert c.max_q_len == 2 ** 31 - 1 and c.max_kv_len == 64
+    big = W.KVBatch(i32(3, 4), i32(4), i32(3), 1, bound)
+    assert big._for(cache)._obj.max_kv_len == 2 ** 31 - 1  # more than the table holds, which the C calls refuse
+    assert W.KVBatch(i32(3, 4), i32(4), i32(3), -bound)._for(cache)._obj.max_q_len == -2 ** 31  # refused too
+    assert W.w8a8_kv_attention_workspace_size(cache, big, 3, bound + 4) == 0
+
+
+@pytest.mark.parametrize("window,handed", [(7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1),
+                                           (-1, -1), (-2 ** 32, -2 ** 31)])
+def test_windows_past_int32_stay_windows(monkeypatch, window, handed):
+    seen = []
+    monkeypatch.setattr(W, "_same_gpu", lambda *a: None)
+    monkeypatch.setattr(W, "w8a8_kv_attention_workspace_size", lambda *a: 0)
+    monkeypatch.setattr(W, "_kv_call", lambda fn, dev, stream, *args: seen.append(args[7]._obj.window))
+    q = torch.zeros((3, 4, 64), dtype=torch.bfloat16)
+    W.w8a8_kv_attention(q, W.PagedKVCache.empty(4, 2, 16, 64, "cpu"), W.KVBatch(i32(3, 4), i32(4), i32(3), 1), window=window)
+    assert seen == [handed]
+    with pytest.raises(TypeError):
+        W.w8a8_kv_attention(q, W.PagedKVCache.empty(4, 2, 16, 64, "cpu"), W.KVBatch(i32(3, 4), i32(4), i32(3), 1), window=2.5)
