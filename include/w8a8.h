@@ -507,6 +507,11 @@ typedef struct w8a8_kv_batch {
  *   q_out   device bf16 [tokens, q_heads, head_dim] dense, 16-byte aligned;
  *           may be q itself when q is dense
  * Nothing is written for tokens == 0. max_kv_len bounds kv_len as above.
+ * A call of more than 2^31 - 1 blocks is refused with
+ * W8A8_ERR_UNSUPPORTED_SHAPE. With more than 8 new tokens a sequence a block
+ * has one of the 2 * kv_heads * (tokens / page_size + 2 * batch) places for a
+ * page of a head of k or v (8 of them for pages of 16), else 8 of the
+ * 2 * kv_heads * batch.
  */
 w8a8_status w8a8_kv_append(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch, int64_t tokens, const void *k,
                            int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
@@ -526,7 +531,8 @@ w8a8_status w8a8_kv_append(const w8a8_kv_cache *cache, const w8a8_kv_batch *batc
  *               keep what they held.
  * A sequence whose rows pass `rows`, or whose positions are not all in
  * [0, max_pages * page_size), is skipped (W8A8_ERR_BAD_SEQUENCE, which a
- * descending row_start also sets).
+ * descending row_start also sets). kv_heads * (rows / 16 + 2 * batch) of 2^34 - 8
+ * or more is refused with W8A8_ERR_UNSUPPORTED_SHAPE.
  */
 w8a8_status w8a8_kv_gather(const w8a8_kv_cache *cache, const int32_t *page_table, int64_t page_table_ld, int32_t batch,
                            int32_t max_pages, const int32_t *first_pos, const int32_t *row_start, int64_t rows,

@@ -155,6 +155,7 @@ struct KvAppendArgs {
   uint16_t *q_out = nullptr;
   int32_t *status = nullptr;
 };
+bool kv_append_fits(const KvAppendArgs &a);  // into a grid's 2^31 - 1 blocks
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
 
 struct KvGatherArgs {
@@ -167,6 +168,7 @@ struct KvGatherArgs {
   void *k_out = nullptr, *v_out = nullptr;
   int32_t *status = nullptr;
 };
+bool kv_gather_fits(const KvGatherArgs &a);  // as kv_append_fits
 cudaError_t launch_kv_gather(const KvGatherArgs &a, bool bf16_out, cudaStream_t s);
 
 struct KvAttnArgs {

@@ -189,6 +189,7 @@ w8a8_status w8a8_kv_append(const w8a8_kv_cache *cache, const w8a8_kv_batch *batc
   a.sin = sin;
   a.rot = cos ? rot_dim : 0;
   a.interleaved = interleaved != 0;
+  if (!kv_append_fits(a)) return W8A8_ERR_UNSUPPORTED_SHAPE;
   a.len_limit = cos && rope_len < a.s.max_kv ? static_cast<int32_t>(rope_len) : a.s.max_kv;
   int sms = 0;
   if (w8a8_status s = current_device_info(&sms, &a.status)) return s;
@@ -217,6 +218,7 @@ w8a8_status w8a8_kv_gather(const w8a8_kv_cache *cache, const int32_t *page_table
   a.rows = rows;
   a.k_out = k_out;
   a.v_out = v_out;
+  if (!kv_gather_fits(a)) return W8A8_ERR_UNSUPPORTED_SHAPE;
   int sms = 0;
   if (w8a8_status s = current_device_info(&sms, &a.status)) return s;
   return from_cuda(launch_kv_gather(a, out_dtype == W8A8_BF16, static_cast<cudaStream_t>(stream)));

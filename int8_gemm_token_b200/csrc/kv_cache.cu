@@ -350,22 +350,30 @@ int64_t query_warps(const KvAppendArgs &a) {
   return a.q_out ? a.s.tokens * ((a.q_heads + query_heads<D>() - 1) / query_heads<D>()) : 0;
 }
 
+// Threads of a page's unit (append_pages_kernel's G), and slots of pages.
+int page_threads(const KvAppendArgs &a) { return 2 * a.c.page; }
+int64_t page_slots(const KvAppendArgs &a) { return (a.s.tokens >> a.c.page_shift) + 2 * static_cast<int64_t>(a.s.batch); }
+int page_block(const KvAppendArgs &a) { return page_threads(a) > 32 ? page_threads(a) : kThreads; }
+
+template <int D>
+int64_t append_blocks(const KvAppendArgs &a) {
+  const int64_t heads = static_cast<int64_t>(a.c.heads) * 2;
+  if (a.s.max_q <= kFewTokens) return (a.s.batch * heads + query_warps<D>(a) + kThreads / 32 - 1) / (kThreads / 32);
+  return (page_slots(a) * heads * page_threads(a) + query_warps<D>(a) * 32 + page_block(a) - 1) / page_block(a);
+}
+
 template <int D, int G>
 cudaError_t launch_pages_t(const KvAppendArgs &a, cudaStream_t s) {
-  constexpr int BLOCK = G > 32 ? G : kThreads;
-  const int64_t tiles = (a.s.tokens >> a.c.page_shift) + 2 * static_cast<int64_t>(a.s.batch);
-  const int64_t threads = tiles * a.c.heads * 2 * G + query_warps<D>(a) * 32;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = pdl_config((threads + BLOCK - 1) / BLOCK, BLOCK, s, &attr);
-  return cudaLaunchKernelEx(&cfg, append_pages_kernel<D, G>, a, tiles);
+  const cudaLaunchConfig_t cfg = pdl_config(append_blocks<D>(a), G > 32 ? G : kThreads, s, &attr);
+  return cudaLaunchKernelEx(&cfg, append_pages_kernel<D, G>, a, page_slots(a));
 }
 
 template <int D>
 cudaError_t launch_append_t(const KvAppendArgs &a, cudaStream_t s) {
   if (a.s.max_q <= kFewTokens) {
-    const int64_t warps = static_cast<int64_t>(a.s.batch) * a.c.heads * 2 + query_warps<D>(a);
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = pdl_config((warps + kThreads / 32 - 1) / (kThreads / 32), kThreads, s, &attr);
+    const cudaLaunchConfig_t cfg = pdl_config(append_blocks<D>(a), kThreads, s, &attr);
     return cudaLaunchKernelEx(&cfg, append_few_kernel<D>, a);
   }
   switch (a.c.page) {
@@ -460,9 +468,11 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   }
 }
 
+int64_t gather_warps(const KvGatherArgs &a) { return (a.rows / kGran + 2 * static_cast<int64_t>(a.batch)) * a.c.heads; }
+
 template <int D>
 cudaError_t launch_gather_t(const KvGatherArgs &a, bool bf16_out, cudaStream_t s) {
-  const int64_t warps = (a.rows / kGran + 2 * static_cast<int64_t>(a.batch)) * a.c.heads;
+  const int64_t warps = gather_warps(a);
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = pdl_config((warps + kThreads / 32 - 1) / (kThreads / 32), kThreads, s, &attr);
   if (bf16_out) return cudaLaunchKernelEx(&cfg, gather_kernel<D, true>, a, warps);
@@ -470,6 +480,13 @@ cudaError_t launch_gather_t(const KvGatherArgs &a, bool bf16_out, cudaStream_t s
 }
 
 }  // namespace
+
+bool kv_append_fits(const KvAppendArgs &a) {
+  const int64_t blocks = a.c.d == 64 ? append_blocks<64>(a) : a.c.d == 96 ? append_blocks<96>(a) : append_blocks<128>(a);
+  return blocks <= INT32_MAX;
+}
+
+bool kv_gather_fits(const KvGatherArgs &a) { return gather_warps(a) / (kThreads / 32) < INT32_MAX; }
 
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s) {
   switch (a.c.d) {

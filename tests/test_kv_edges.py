@@ -1,9 +1,11 @@
 """What the binding of the INT8 paged KV cache hands to the C calls, on a host
-without a GPU: row strides of page tables, bounds of any size."""
+without a GPU: row strides of page tables, bounds of any size; and
+calls whose grids would pass what a launch holds."""
 import pytest
 import torch
 
 from int8_gemm_token_b200 import w8a8 as W
+from tests.test_kv_cache import append, batch, cache, gather
 
 
 def i32(*shape):
@@ -67,3 +69,29 @@ def test_windows_past_int32_stay_windows(monkeypatch, window, handed):
     assert seen == [handed]
     with pytest.raises(TypeError):
         W.w8a8_kv_attention(q, W.PagedKVCache.empty(4, 2, 16, 64, "cpu"), W.KVBatch(i32(3, 4), i32(4), i32(3), 1), window=2.5)
+
+
+# ------------------------------------------------------------------ grids past 2^31 - 1 blocks
+def test_appends_of_more_blocks_than_a_launch_holds_are_refused():
+    """They would have been cut to the count's low 32 bits, or not been launched at all."""
+    plain = dict(cos=None, sin=None, q=None, qo=None)
+    wide = dict(c=cache(heads=65535, page=128, d=64), tokens=9)
+    # 9 new tokens: a block of 256 threads for each slot of a page, head and of k and v, two slots a sequence
+    for n in (8193, 16384, 65535):  # 2^31 blocks and a little more; about 2^32, whose low bits are few; the largest batch
+        assert append(b=batch(batch=n, max_q=9), **wide, **plain) == 3
+    # query rows: a warp for each 32 heads of 64, 8 of them a block
+    assert append(c=cache(d=64), tokens=1 << 30, hq=65535, b=batch(max_q=8), cos=None, sin=None) == 3
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses")
+def test_appends_of_fewer_blocks_are_taken():
+    plain = dict(cos=None, sin=None, q=None, qo=None)
+    wide = dict(c=cache(heads=65535, page=128, d=64), tokens=9)
+    assert append(b=batch(batch=8192, max_q=9), **wide, **plain) == 10  # no device here
+    assert append(b=batch(batch=65535, max_q=8), **wide, **plain) == 10  # a warp for each sequence, head and of k and v
+    assert gather(c=cache(heads=65535), rows=1 << 20) == 10
+
+
+def test_read_backs_of_more_blocks_than_a_launch_holds_are_refused():
+    assert gather(c=cache(heads=65535), rows=1 << 30) == 3
+    assert gather(c=cache(heads=1 << 14, d=64), rows=1 << 24, n=60000) == 3
