@@ -28,3 +28,16 @@ def read_golden(name):
 @pytest.fixture(scope="session")
 def golden():
     return read_golden
+
+
+# Tests without a GPU that also make a good call with made-up addresses, which only a host without a device refuses:
+# where a GPU is current its kernel would run on them.
+NO_DEVICE_ONLY = {"test_kv_cache.py::test_append_refusals"}
+
+
+def pytest_collection_modifyitems(items):
+    import torch
+    if torch.cuda.is_available():
+        for item in items:
+            if item.nodeid.rpartition("/")[2] in NO_DEVICE_ONLY:
+                item.add_marker(pytest.mark.skip(reason="made-up addresses"))

@@ -95,3 +95,24 @@ def test_appends_of_fewer_blocks_are_taken():
 def test_read_backs_of_more_blocks_than_a_launch_holds_are_refused():
     assert gather(c=cache(heads=65535), rows=1 << 30) == 3
     assert gather(c=cache(heads=1 << 14, d=64), rows=1 << 24, n=60000) == 3
+
+
+# ------------------------------------------------------------------ made-up addresses stay on hosts without a GPU
+def test_good_calls_with_made_up_addresses_are_skipped_where_a_gpu_is(monkeypatch):
+    """test_append_refusals begins with one, whose kernel a GPU would run."""
+    from tests import conftest
+
+    class Item:
+        def __init__(self, nodeid):
+            self.nodeid, self.marks = nodeid, []
+
+        def add_marker(self, mark):
+            self.marks.append(mark.name)
+
+    ids = ["tests/test_kv_cache.py::test_append_refusals", "test_kv_cache.py::test_append_refusals",
+           "tests/test_kv_cache.py::test_gather_refusals"]
+    for gpu, want in ((True, [["skip"], ["skip"], []]), (False, [[], [], []])):
+        monkeypatch.setattr(torch.cuda, "is_available", lambda gpu=gpu: gpu)
+        items = [Item(i) for i in ids]
+        conftest.pytest_collection_modifyitems(items)
+        assert [i.marks for i in items] == want
