@@ -497,11 +497,23 @@ class _ScoresStruct(ctypes.Structure):
     _fields_ = [("scale", _F), ("softcap", _F), ("slopes", _P), ("window", _I32), ("prefix_len", _P)]
 
 
-class PagedKVCache:
+class _Described:
+    """What the C calls get is taken from the attributes once, when the object
+    is made. So those cannot be assigned again: the calls would not see it."""
+
+    _taken = frozenset()
+
+    def __setattr__(self, name, value):
+        if name in self._taken:
+            raise AttributeError(f"{type(self).__name__}.{name} was taken when the object was made: make another one")
+        object.__setattr__(self, name, value)
+
+
+class PagedKVCache(_Described):
     """An INT8 paged KV cache (w8a8_kv_cache): codes int8 [pages, kv_heads,
     page_size, head_dim] and scales fp32 [pages, kv_heads], for keys and for
     values. Checked once here; keeps the tensors alive. Their contents may
-    change between calls, the tensors may not be resized."""
+    change between calls, the tensors may be neither resized nor exchanged."""
 
     def __init__(self, k_codes, v_codes, k_scale, v_scale):
         if not isinstance(k_codes, torch.Tensor) or k_codes.dtype != torch.int8 or k_codes.dim() != 4:
@@ -523,6 +535,7 @@ class PagedKVCache:
             raise ValueError(f"expected tensors on one device, got {sorted({str(t.device) for t in self._tensors})}")
         self._c = _CacheStruct(*(t.data_ptr() for t in self._tensors), *shape)
         self._ref = ctypes.byref(self._c)
+        self._taken = frozenset(vars(self))
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, device=None):
@@ -552,12 +565,12 @@ def _page_table(t) -> int:
     return t.shape[1]
 
 
-class KVBatch:
+class KVBatch(_Described):
     """The sequences of a call (w8a8_kv_batch): page_table int32 [batch,
     max_pages] (rows contiguous, at any distance that keeps them apart),
     seq_start int32 [batch + 1], kv_len int32 [batch], all on the device and
     read there, and the host's bounds on a sequence's new tokens and length.
-    Checked once here."""
+    Checked once here; as of a PagedKVCache, only the tensors' contents may change."""
 
     def __init__(self, page_table, seq_start, kv_len, max_q_len: int, max_kv_len: int | None = None):
         ld = _page_table(page_table)
@@ -572,6 +585,7 @@ class KVBatch:
         self._fields = (page_table.data_ptr(), ld, seq_start.data_ptr(), kv_len.data_ptr(), batch, max_pages,
                         self.max_q_len)
         self._refs = {}
+        self._taken = frozenset(vars(self))
 
     def _for(self, cache: PagedKVCache):
         """The C struct for caches of that page size, with the longest length

@@ -116,3 +116,19 @@ def test_good_calls_with_made_up_addresses_are_skipped_where_a_gpu_is(monkeypatc
         items = [Item(i) for i in ids]
         conftest.pytest_collection_modifyitems(items)
         assert [i.marks for i in items] == want
+
+
+# ------------------------------------------------------------------ what was checked once stays what it was
+def test_caches_and_batches_cannot_be_given_other_tensors():
+    """The addresses were taken when the object was made: another tensor would not be looked at."""
+    c, b = W.PagedKVCache.empty(4, 2, 16, 64, "cpu"), W.KVBatch(i32(3, 4), i32(4), i32(3), 1)
+    for obj, names in ((c, ("k_codes", "v_codes", "k_scale", "v_scale", "page_size", "num_pages")),
+                       (b, ("page_table", "seq_start", "kv_len", "max_q_len", "max_kv_len"))):
+        for name in names:
+            was = getattr(obj, name)
+            with pytest.raises(AttributeError, match=name):
+                setattr(obj, name, torch.ones_like(was) if isinstance(was, torch.Tensor) else 7)
+            assert getattr(obj, name) is was
+    b.kv_len.fill_(5)  # the contents may change
+    b.note = "anything else is the caller's"
+    b.note = "and stays so"
