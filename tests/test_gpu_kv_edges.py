@@ -1,5 +1,6 @@
 """The INT8 paged KV cache on the GPU at its edges: table entries that no call
-needs, ranges of nothing, weights far below a row's largest."""
+needs, ranges of nothing, weights far below a row's largest, bounds
+far above the lengths, captured chunks."""
 import numpy as np
 import pytest
 import torch
@@ -8,7 +9,7 @@ from int8_gemm_token_b200 import synth
 from int8_gemm_token_b200 import w8a8 as W
 from tests import kv_reference as R
 from tests.gpu_util import dev, dev_bf16, host_bf16
-from tests.test_gpu_kv_cache import batch_of, bf16_rows, status, to_dev
+from tests.test_gpu_kv_cache import batch_of, bf16_rows, check_attention, mask_args, status, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +114,59 @@ def test_small_weights_of_many_keys_add_up(B, hq, n, log2_weight):
     tol = n * 2.0 ** -32 + want * (2.0 ** -8 + T / 8 + 2.0 ** -13)
     assert (np.abs(got - want) <= tol).all(), (got.min(), got.max(), want, tol)
     assert status() == 0
+
+
+# ------------------------------------------------------------------ bounds that say little
+@pytest.mark.parametrize("mask", ["plain", "window_prefix", "all"])
+@pytest.mark.parametrize("d,page,hq,hkv", [(128, 64, 8, 2), (64, 16, 4, 4), (96, 32, 16, 1)])
+@pytest.mark.parametrize("new", [(1, 1, 1), (3, 1, 2), (200, 1, 1), (1, 70, 300)])
+def test_tables_much_wider_than_the_contexts(d, page, hq, hkv, new, mask):
+    """The bound that a table of 40000 positions implies chooses kernels and sizes the workspace, and a batch may mix
+    chunks with single tokens."""
+    rng = np.random.default_rng(new[0] + d)
+    s, pages = R.make_seqs(rng, list(new), [40, 500, 0], page, spare=1, width_extra=40000 // page)
+    check_attention(rng, s, R.random_cache(rng, pages, hkv, page, d), hq, **mask_args(mask, hq))
+
+
+# ------------------------------------------------------------------ many rows in a graph
+def test_a_captured_chunk_follows_its_lengths():
+    """One captured call (append, attention) of up to 260 new tokens a sequence, replayed for chunks of other lengths,
+    equals eager calls."""
+    rng = np.random.default_rng(8)
+    page, hkv, hq, d, B, rows, most, bound = 16, 2, 8, 128, 3, 420, 260, 800
+    table = dev(rng.permutation(B * bound // page).astype(np.int32).reshape(B, -1))
+    base = R.random_cache(rng, B * bound // page, hkv, page, d)
+    chunks = [([130, 1, 260], [0, 40, 17]), ([260, 160, 0], [540, 0, 300]), ([1, 1, 1], [799, 0, 31]), ([0, 0, 0], [5, 9, 0]),
+              ([99, 200, 121], [3, 600, 256])]
+    start, kv = dev(np.zeros(B + 1, np.int32)), dev(np.zeros(B, np.int32))
+    caches = [to_dev(base), to_dev(base)]
+    batch = W.KVBatch(table, start, kv, most, bound)
+    cos, sin = (dev(x) for x in R.angles(bound, d))
+    x = torch.zeros((rows, hq + 2 * hkv, d), dtype=torch.bfloat16, device="cuda")
+    n = W.w8a8_kv_attention_workspace_size(caches[0], batch, rows, hq)
+    ws = [torch.empty((n,), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs, qs = ([torch.empty((rows, hq, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)] for _ in range(2))
+
+    def step(i):
+        W.w8a8_kv_append(x[:, hq:hq + hkv], x[:, hq + hkv:], caches[i], batch, cos, sin, q=x[:, :hq], q_out=qs[i])
+        W.w8a8_kv_attention(qs[i], caches[i], batch, out=outs[i], workspace=ws[i])
+
+    step(0)  # (no new tokens)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(0)
+    for new, ctx in chunks:
+        start.copy_(torch.from_numpy(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)))
+        kv.copy_(torch.from_numpy(np.array(new, np.int32) + np.array(ctx, np.int32)))
+        x.copy_(dev_bf16(bf16_rows(rng, rows, hq + 2 * hkv, d)))
+        for t in (*outs, *qs):
+            t.fill_(7.0)
+        graph.replay()
+        step(1)
+        assert torch.equal(outs[0], outs[1]) and torch.equal(qs[0], qs[1]), new
+        assert (outs[0][sum(new):] == 7).all() and torch.isfinite(outs[0]).all()
+        for a, b in zip(caches[0]._tensors, caches[1]._tensors):
+            assert torch.equal(a, b)
+    assert status() == 0
+    graph.reset()
