@@ -543,7 +543,9 @@ typedef struct w8a8_kv_scores {
   float scale;               /* multiplies q . k; finite */
   float softcap;             /* > 0: scores become softcap * tanh(score / softcap), at most 4096 and with
                                 scale / softcap finite; 0: none */
-  const float *slopes;       /* device fp32 [q_heads] or NULL: adds -slopes[h] * (distance of query and key) */
+  const float *slopes;       /* device fp32 [q_heads] or NULL: adds -slopes[h] * (p - j), p the query's position and j
+                                the key's: linear in j, so for the keys in front of the query that a prefix opens it
+                                is a bonus that grows with their distance */
   int32_t window;            /* > 0: only keys less than `window` positions before the query; 0: no limit */
   const int32_t *prefix_len; /* device int32 [batch] or NULL: keys at positions below it are seen by every query */
 } w8a8_kv_scores;
@@ -557,13 +559,16 @@ typedef struct w8a8_kv_scores {
  *   out[t, h] = sum_j softmax(s)_j v_j       (0 for a padding row, p < 0)
  * k_j and v_j are the values the codes stand for; scores, the running maximum
  * and sum and the accumulation are fp32. Rounding: the codes enter the tensor
- * cores exactly (an int8 code is exact in fp16 and in bf16) and so does q; the
- * page's scales are applied in fp32. The weights times v's scale are rounded
- * once for the second product, by the query rows of a kv head (max_q_len *
- * (q_heads / kv_heads)): for up to 32, and up to 64 where batch * kv_heads <= 64
- * or max_kv_len >= 4096, to fp16 against the row's largest (2^-11 of the value,
- * at least 2^-32 of the largest); for more to bf16 (2^-8 of the value). A
- * capped score is off by about softcap * 2^-22.
+ * cores exactly (an int8 code is exact in fp16 and in bf16); the page's scales
+ * are applied in fp32. The rest goes by the query rows of a kv head (max_q_len *
+ * (q_heads / kv_heads)): "few" are up to 32, and up to 64 where batch * kv_heads
+ * <= 64 or max_kv_len >= 4096. q enters exactly, except that with few rows an
+ * element below 2^-31 of its row's largest is rounded to a multiple of 2^-39 of
+ * it. The weights times v's scale are rounded once for the second product: with
+ * few rows to fp16 against the row's largest (2^-11 of the value,
+ * at least 2^-32 of the largest); else to bf16 (2^-8 of the value). A weight
+ * below 2^-126 of the row's largest, or with many rows a product below 2^-126,
+ * may become 0. A capped score is off by about softcap * 2^-22.
  *   q      device bf16 [tokens, q_heads, head_dim], strides in elements
  *          (multiples of 8, and not 0 where the axis has several elements)
  *   out    device bf16 [tokens, q_heads, head_dim] dense, 16-byte aligned
@@ -598,7 +603,15 @@ w8a8_status w8a8_kv_attention_requant(const w8a8_kv_cache *cache, const w8a8_kv_
                                       int8_t *codes_out, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of device workspace the two attention calls need on the current
- * device (0 for arguments they refuse, and where they need none). */
+ * device (0 for arguments they refuse, and where they need none). With few
+ * query rows of a kv head (as above) 20 MiB at most. With many it goes by the
+ * bounds, not by the lengths:
+ *   batch * kv_heads * (max_kv_len rounded up to 128)
+ *     * (512.5 bytes, or 256.5 at head_dim 64),
+ * at most 2 KiB * (head_dim + 2) for each SM, and the list of query blocks. So
+ * does a part of the time (a launch over the same keys): a max_kv_len near the
+ * longest length, and calls of their own for prompt chunks and for single
+ * tokens, which otherwise take the path of the chunks, cost the least. */
 size_t w8a8_kv_attention_workspace_size(const w8a8_kv_cache *cache, const w8a8_kv_batch *batch, int64_t tokens,
                                         int32_t q_heads);
 

@@ -267,7 +267,7 @@ __device__ __forceinline__ void rotate_query_rows(const KvAppendArgs &a, int64_t
 }
 
 // Few new tokens a sequence: warps [0, batch * heads * 2) one (sequence,
-// head, k or v) each, the following warps one query row each.
+// head, k or v) each, the following warps a block of heads of a query row each.
 template <int D>
 __global__ void __launch_bounds__(kThreads) append_few_kernel(const __grid_constant__ KvAppendArgs a) {
   pdl_launch_dependents();

@@ -18,7 +18,7 @@
 // subtracted (per four codes one xor, two byte permutes, two packed adds).
 //   fp16 has the codes' bits to spare but not bf16's range, so what meets them
 // is scaled by powers of two, exactly: a query row so that its largest
-// element is in [2^14, 2^15) (elements 2^-29 below it start to lose bits), and
+// element is in [2^14, 2^15) (elements below 2^-31 of it lose bits), and
 // the weights 2^s_j times v's scale against a running reference of their own,
 // apart from that of the scores:
 //   w_j = 2^(s_j + log2 vs_j - mv + 7),  l = sum_j 2^(s_j - m) in fp32,
@@ -55,15 +55,16 @@
 // few and short a block has a segment, and there is nothing to join: one
 // launch. The rules and what they measured stand at the host's choice below.
 //
-// Measured (device time, back to back): 32 sequences x 32 heads x 4096 keys of
-// 128 (1.07 GB of codes) 189 to 193 us, 5.6 TB/s; 64 sequences of 1 to 32768
-// keys, 8 heads for 32 (547 MB) 103 us, 5.3 TB/s: the rate of a stream that is
-// only read (5.3 to 5.7 TB/s here, where a copy moves 6.6). Alone in a profile
-// the first takes 168 us: the SMs issue in 57 % of cycles, the ALU pipe in
-// 51 %, the tensor pipe is 20 % busy. Scores by s8 products (codes as they lie,
-// q as 22-bit fixed point in three int8 parts) need a sixth fewer
-// instructions and measured 192 to 202 and 103.5 us: not the limit. The
-// smallest calls are their latency: one sequence of 512 keys 8.0 us.
+// Measured: 32 sequences x 32 heads x 4096 keys of 128 (1.07 GB of codes) alone
+// in a profile 168 us, 6.4 TB/s, DRAM 79 % busy; the SMs issue in 57 % of cycles,
+// the ALU pipe in 51 %, the tensor pipe is 20 % busy. Back to back for seconds
+// the board is at its power cap and the time goes with the clock: 178.5 us at
+// 1725 MHz on one, 191 at 1612 on another (0.308 s MHz both), 5.6 to 6.0 TB/s. 64
+// sequences of 1 to 32768 keys, 8 heads for 32 (547 MB): 103 us, 5.3 TB/s.
+// Scores by s8 products (codes as they lie, q as 22-bit fixed point in three
+// int8 parts) need a sixth fewer instructions and measured 192 to 202 and
+// 103.5 us where this took 189 to 193 and 102.7: instructions are not the limit.
+// The smallest calls are their latency: one sequence of 512 keys 8.0 us.
 #include "kv_common.cuh"
 
 namespace w8a8 {

@@ -51,9 +51,14 @@
 // against 445. Sixteen softmax warps: 96 registers each are too few for the
 // row, slower. Some of the exponentials as polynomials on the FMA pipe:
 // slower from the first element on.
-// Measured (device time, both kernels, 32 heads of 128): a prompt of 2048
-// 57 us, of 8192 445 to 465 us (550 GFLOP, 1.2 PFLOP/s; 0.71 to 0.74 of the rate
-// of a large bf16 product).
+// Measured (device time, both kernels, 32 heads of 128): a prompt of 2048 59 us;
+// of 8192 (550 GFLOP) 449 us at 1965 MHz, 1.22 PFLOP/s and 0.73 of the rate of a
+// large bf16 product in a short run, but 515 at the power cap's 1687 MHz after
+// seconds (0.88 and 0.87 s MHz), 0.76 of what such a product keeps up there.
+//   The weights are bf16 because they carry v's scales, whose range fp16 has
+// only against a reference for each row, which kv_decode.cu keeps and which
+// would cost this kernel a second running maximum. Against a 64-bit evaluation
+// the output is off by 0.0023 to 0.0026 where its own rounding to bf16 is 0.0017.
 #include <type_traits>
 
 #include "kv_common.cuh"

@@ -569,8 +569,11 @@ class KVBatch(_Described):
     """The sequences of a call (w8a8_kv_batch): page_table int32 [batch,
     max_pages] (rows contiguous, at any distance that keeps them apart),
     seq_start int32 [batch + 1], kv_len int32 [batch], all on the device and
-    read there, and the host's bounds on a sequence's new tokens and length.
-    Checked once here; as of a PagedKVCache, only the tensors' contents may change."""
+    read there, and the host's bounds on a sequence's new tokens and length
+    (without max_kv_len what the table holds; attention of many new tokens
+    takes workspace for batch * kv_heads * max_kv_len keys, see
+    w8a8_kv_attention_workspace_size in the header). Checked once here; as of
+    a PagedKVCache, only the tensors' contents may change."""
 
     def __init__(self, page_table, seq_start, kv_len, max_q_len: int, max_kv_len: int | None = None):
         ld = _page_table(page_table)
@@ -673,7 +676,8 @@ def w8a8_kv_append(k, v, cache: PagedKVCache, batch: KVBatch, cos=None, sin=None
                    interleaved: bool = False, stream=None):
     """Rotate (cos, sin fp32 [positions, rot_dim / 2]), quantize and store the
     new tokens' keys and values; with q, rotate the queries into q_out (bf16
-    [tokens, q_heads, head_dim], allocated when None; returned)."""
+    [tokens, q_heads, head_dim], allocated when None, and then uninitialised in
+    rows of no sequence; returned)."""
     d, dev = cache.head_dim, cache._dev
     tokens, _, kst, ksh = _heads3(k, cache.kv_heads, d, "k")
     _, _, vst, vsh = _heads3(v, cache.kv_heads, d, "v", tokens)
@@ -713,7 +717,7 @@ def w8a8_kv_gather(cache: PagedKVCache, page_table, first_pos, row_start, rows: 
     """Read positions first_pos[b] .. of each sequence back into rows
     row_start[b] .. row_start[b + 1] of k_out and v_out [rows, kv_heads,
     head_dim] (bf16 or fp32; both allocated for `rows` rows when neither is
-    given) -> (k_out, v_out)."""
+    given, and then uninitialised in rows of no sequence) -> (k_out, v_out)."""
     ld = _page_table(page_table)
     batch, max_pages = page_table.shape
     _dense(first_pos, torch.int32, (batch,), "first_pos")
@@ -784,7 +788,9 @@ def w8a8_kv_attention(q, cache: PagedKVCache, batch: KVBatch, scale: float | Non
                       window: int = 0, slopes=None, prefix_len=None, out=None, workspace=None, stream=None):
     """Causal attention of bf16 q [tokens, q_heads, head_dim] over the cache ->
     bf16 of the same shape (rows of no sequence are left as they are in a
-    given `out`). scale defaults to head_dim ** -0.5."""
+    given `out`, and uninitialised in one that is allocated here; so are those
+    of a sequence that is skipped). scale defaults to head_dim ** -0.5; slopes
+    [q_heads] add -slope * (query's position - key's)."""
     return _attention("w8a8_kv_attention", q, cache, batch, scale, softcap, window, slopes, prefix_len, out,
                       torch.bfloat16, (), workspace, stream)
 
@@ -793,7 +799,8 @@ def w8a8_kv_attention_requant(q, cache: PagedKVCache, batch: KVBatch, r_out, Z_o
                               softcap: float = 0.0, window: int = 0, slopes=None, prefix_len=None, out=None,
                               workspace=None, stream=None):
     """w8a8_kv_attention whose bf16 result is quantized at once with the output
-    projection's static r_out, Z_out: returns int8 [tokens, q_heads, head_dim]."""
+    projection's static r_out, Z_out: returns int8 [tokens, q_heads, head_dim]
+    (rows of no sequence as there)."""
     _vec(r_out, torch.float32, 1, "r_out")
     _vec(Z_out, torch.int32, 1, "Z_out")
     return _attention("w8a8_kv_attention_requant", q, cache, batch, scale, softcap, window, slopes, prefix_len, out,
